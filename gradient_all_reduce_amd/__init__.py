@@ -10,6 +10,7 @@ module raises ImportError on import.
 torch is imported before the library is loaded so that the library binds to
 the HIP runtime torch already loaded (one runtime, one device context).
 """
+import collections
 import ctypes
 import os
 
@@ -29,6 +30,9 @@ __all__ = [
     "gb_encode", "gb_decode_sum", "gb_bucket_allreduce_local_typed", "gb_reduce_encode",
     "gb_bucket_allreduce_local_batch", "gb_bucket_allreduce_local_batch_ef", "gb_bucket_batch_workspace_bytes",
     "GB_MAX_BATCH", "gb_bucket_allreduce_local_noalloc", "GB_NOALLOC_SCRATCH_BYTES",
+    "GB_STATE_F32", "GB_STATE_E4M3", "GB_OPTIM_CONTROL_BYTES", "GB_OPTIM_MAX_TENSORS", "GbOptimTensor", "GbOptimPlan",
+    "gb_optim_plan_bytes", "gb_optim_plan", "gb_optim_control", "gb_optim_begin", "gb_optim_begin_clip",
+    "gb_adamw_step",
 ]
 
 GB_OK, GB_ERR_INVALID_ARG, GB_ERR_MISALIGNED = 0, 1, 2
@@ -41,6 +45,9 @@ GB_MAX_K = 16
 GB_MAX_N = 1 << 39  # largest element count a call accepts
 GB_MAX_BATCH = 4096  # largest bucket count of gb_bucket_allreduce_local_batch
 GB_NOALLOC_SCRATCH_BYTES = 64 << 20  # static payload scratch of gb_bucket_allreduce_local_noalloc
+GB_STATE_F32, GB_STATE_E4M3 = 0, 1
+GB_OPTIM_CONTROL_BYTES = 64  # the control block of the optimizer step
+GB_OPTIM_MAX_TENSORS = 65536  # largest number of tensors of a plan
 # gb_dtype of each torch element type gb_reduce_typed takes
 GB_DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float64: 3,
             torch.int8: 4, torch.uint8: 5, torch.int32: 6, torch.int64: 7}
@@ -58,6 +65,21 @@ _lib = ctypes.CDLL(library_path)
 _P, _S, _I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _PP = ctypes.POINTER(ctypes.c_void_p)
 _SP = ctypes.POINTER(ctypes.c_size_t)
+
+
+class _OptimTensor(ctypes.Structure):
+    """gb_optim_tensor of include/gbreduce.h."""
+    _fields_ = [("n", _S), ("param", _P), ("grad", _P), ("copy", _P), ("m", _P), ("v", _P), ("m_scale", _P),
+                ("v_scale", _P), ("dtype", _I), ("state", _I), ("lr_scale", ctypes.c_float),
+                ("weight_decay", ctypes.c_float)]
+
+
+class _OptimHandle(ctypes.Structure):
+    """gb_optim_handle of include/gbreduce.h."""
+    _fields_ = [("opaque", ctypes.c_uint64 * 24)]
+
+
+_D = ctypes.c_double
 _SIGNATURES = {
     "gb_reduce_sum": (_I, [_P, _PP, _I, _S, _P]),
     "gb_reduce": (_I, [_P, _PP, _I, _S, _I, _I, _P]),
@@ -81,6 +103,11 @@ _SIGNATURES = {
     "gb_bucket_allreduce_local_ef_typed": (_I, [_I, _P, _PP, _PP, _I, _S, _S, _I, _I, _P, _S, _P]),
     "gb_encode_staged": (_I, [_I, _I, _P, _P, _P, _P, _P, _S, _S, _P]),
     "gb_decode_accumulate_staged": (_I, [_P, _PP, _PP, _PP, _PP, _I, _S, _S, _I, _I, _P]),
+    "gb_optim_plan_bytes": (_S, [_SP, _I]),
+    "gb_optim_plan": (_I, [_P, _P, _I, _D, _D, _D, ctypes.c_uint64, _P, _S, _P]),
+    "gb_optim_begin": (_I, [_P, _P, _D, _P]),
+    "gb_optim_begin_clip": (_I, [_P, _P, _D, _D, _P]),
+    "gb_adamw_step": (_I, [_P, _P, _P]),
     "gb_payload_bytes": (_S, [_I, _S]),
     "gb_bucket_workspace_layout": (_I, [_I, _I, _S, _S, _SP, _SP, _SP, _SP]),
     "gb_bucket_workspace_bytes": (_S, [_I, _I, _S, _S]),
@@ -531,6 +558,113 @@ def gb_decode_accumulate_staged(acc, codes_host, scales_host, codes_dev, scales_
     _check(_lib.gb_decode_accumulate_staged(_ptr(acc), _ptr_array(codes_host), sh, _ptr_array(codes_dev), sd,
                                             len(codes_host), n, int(chunk_elems), int(codec),
                                             int(bool(accumulate)), _stream(stream, acc.device)))
+
+
+GbOptimTensor = collections.namedtuple(
+    "GbOptimTensor", "param grad m v m_scale v_scale copy lr_scale weight_decay",
+    defaults=(None, None, None, 1.0, 0.0))
+GbOptimTensor.__doc__ = """One tensor of an optimizer plan: param (float32), grad (float32, float16 or
+bfloat16), and the moments: m and v float32, or uint8 E4M3 codes of m and
+sqrt(v) with float32 scales m_scale and v_scale, one per 256 values.  copy
+(float16 or bfloat16, grad's type) receives the updated parameters rounded;
+lr_scale multiplies the control block's learning rate; weight_decay is
+decoupled.  All zeros is the moments' state before the first step."""
+
+
+class GbOptimPlan:
+    """A list of tensors laid out for gb_optim_begin, gb_optim_begin_clip and
+    gb_adamw_step; made by gb_optim_plan, keeps its tensors and workspace."""
+
+    __slots__ = ("handle", "ref", "tensors", "workspace", "device")
+
+    def __init__(self, handle, tensors, workspace):
+        self.handle, self.tensors, self.workspace = handle, tensors, workspace
+        self.ref, self.device = ctypes.byref(handle), workspace.device
+
+
+def gb_optim_plan_bytes(ns):
+    """Workspace bytes of gb_optim_plan over tensors of ns values."""
+    return int(_lib.gb_optim_plan_bytes(_size_array(ns), len(ns)))
+
+
+def _optim_entry(i, t):
+    n = t.param.numel() if isinstance(t.param, torch.Tensor) else 0
+    name = f"tensors[{i}]"
+    _device_tensor(t.param, torch.float32, name + ".param")
+    if not isinstance(t.grad, torch.Tensor) or t.grad.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+        raise TypeError(f"{name}.grad must be a tensor of float32, float16 or bfloat16")
+    _device_tensor(t.grad, t.grad.dtype, name + ".grad")
+    coded = isinstance(t.m, torch.Tensor) and t.m.dtype == torch.uint8
+    for part, dtype in (("m", torch.uint8 if coded else torch.float32), ("v", torch.uint8 if coded else torch.float32)):
+        _device_tensor(getattr(t, part), dtype, f"{name}.{part}")
+        _same_numel([getattr(t, part)], n, f"{name}.{part}")
+    _same_numel([t.grad], n, name + ".grad")
+    for part in ("m_scale", "v_scale"):
+        scale = getattr(t, part)
+        if coded:
+            _device_tensor(scale, torch.float32, f"{name}.{part}")
+            _same_numel([scale], (n + GB_BLOCK - 1) // GB_BLOCK, f"{name}.{part}")
+    if t.copy is not None:
+        _device_tensor(t.copy, t.grad.dtype, name + ".copy")
+        _same_numel([t.copy], n, name + ".copy")
+    ptr = lambda x: x.data_ptr() if x is not None else None  # noqa: E731
+    return _OptimTensor(n, ptr(t.param), ptr(t.grad), ptr(t.copy), ptr(t.m), ptr(t.v), ptr(t.m_scale), ptr(t.v_scale),
+                        GB_DTYPE[t.grad.dtype], GB_STATE_E4M3 if coded else GB_STATE_F32, float(t.lr_scale),
+                        float(t.weight_decay))
+
+
+def gb_optim_plan(tensors, workspace, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, stream=None):
+    """Lay out GbOptimTensors for the step calls; workspace is a uint8 tensor
+    of gb_optim_plan_bytes([t.param.numel() for t in tensors]) bytes, and seed
+    that of the 8-bit moments' dither.  Returns the GbOptimPlan."""
+    tensors = list(tensors)
+    table = (_OptimTensor * max(1, len(tensors)))(*[_optim_entry(i, t) for i, t in enumerate(tensors)])
+    _device_tensor(workspace, torch.uint8, "workspace")
+    for i, t in enumerate(tensors):
+        for part in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy"):
+            x = getattr(t, part)
+            if x is not None and x.device != workspace.device:
+                raise ValueError(f"tensors[{i}].{part} is on {x.device}, the workspace on {workspace.device}")
+    handle = _OptimHandle()
+    _check(_lib.gb_optim_plan(ctypes.byref(handle), table, len(tensors), float(beta1), float(beta2), float(eps),
+                              int(seed) & 0xFFFFFFFFFFFFFFFF, *_workspace_args(workspace),
+                              _stream(stream, workspace.device)))
+    return GbOptimPlan(handle, tensors, workspace)
+
+
+def _control(control):
+    _device_tensor(control, torch.uint8, "control")
+    if control.numel() != GB_OPTIM_CONTROL_BYTES:
+        raise ValueError(f"control has {control.numel()} bytes, expected {GB_OPTIM_CONTROL_BYTES}")
+    return ctypes.c_void_p(control.data_ptr())
+
+
+def gb_optim_control(control):
+    """Views of a control block (GB_OPTIM_CONTROL_BYTES of uint8, zeroed before
+    the first step) by field: step and skipped (int64), lr, norm, coef, rate1
+    and rate2 (float32), skip (int32).  Set lr before the first step:
+    gb_optim_control(control)["lr"].fill_(1e-3)."""
+    _control(control)
+    fields = (("step", 0, torch.int64), ("skipped", 8, torch.int64), ("lr", 16, torch.float32),
+              ("norm", 20, torch.float32), ("coef", 24, torch.float32), ("skip", 28, torch.int32),
+              ("rate1", 32, torch.float32), ("rate2", 36, torch.float32))
+    return {name: control[at:at + (8 if dtype == torch.int64 else 4)].view(dtype) for name, at, dtype in fields}
+
+
+def gb_optim_begin(plan, control, inv_scale=1.0, stream=None):
+    """Open a step: the gradients are scaled by inv_scale (1 / loss scale)."""
+    _check(_lib.gb_optim_begin(plan.ref, _control(control), inv_scale, _stream(stream, plan.device)))
+
+
+def gb_optim_begin_clip(plan, control, max_norm, inv_scale=1.0, stream=None):
+    """Open a step with the global gradient norm, clipped to max_norm; a norm
+    that is not finite skips the step."""
+    _check(_lib.gb_optim_begin_clip(plan.ref, _control(control), max_norm, inv_scale, _stream(stream, plan.device)))
+
+
+def gb_adamw_step(plan, control, stream=None):
+    """The AdamW update of every tensor of the plan, for the step last opened."""
+    _check(_lib.gb_adamw_step(plan.ref, _control(control), _stream(stream, plan.device)))
 
 
 def gb_payload_bytes(codec, n):

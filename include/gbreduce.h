@@ -583,6 +583,148 @@ gb_status gb_decode_accumulate_staged(float* acc, const void* const* codes_host,
                                       size_t chunk_elems, int codec,
                                       int accumulate, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The optimizer step on the reduced gradients: the global gradient norm with
+ * clipping, and AdamW over many tensors at once with its two moments held in
+ * float32 or in 8 bits.  (The pages end with the averaged gradient in the DDP
+ * buckets; these calls take it from there.)
+ *
+ * A plan (gb_optim_plan) lays a list of tensors out once; a step is then two
+ * calls on one stream, whatever the number of tensors:
+ *   gb_optim_begin_clip(&plan, control, max_norm, inv_scale, stream);
+ *       or gb_optim_begin(&plan, control, inv_scale, stream);
+ *   gb_adamw_step(&plan, control, stream);
+ * All that changes from step to step (the step count, the learning rate, the
+ * norm, the factor of the gradients) lies in the control block in device
+ * memory, so the two calls can be captured in a HIP graph and replayed, and
+ * nothing waits for the host.
+ *
+ * Arithmetic, binary32 with every operation rounded on its own, for each
+ * value (g the gradient, p the parameter):
+ *   gs = g * coef
+ *   m' = beta1 * m + (1 - beta1) * gs
+ *   v' = beta2 * v + (1 - beta2) * (gs * gs)
+ *   d  = sqrt(v') * (1 / sqrt(1 - beta2^t)) + eps
+ *   p' = p * (1 - lr_t * weight_decay) - (lr_t * (1 / (1 - beta1^t))) * (m' / d)
+ * with t the step being taken (1 for the first), lr_t = lr * lr_scale of the
+ * tensor; beta1, 1 - beta1, beta2, 1 - beta2, eps and the two bracketed
+ * corrections are computed in binary64 and rounded once to binary32.  A
+ * copy, where the tensor has one, receives p' rounded to its type.  A NaN in
+ * p', m' or v' is stored as 0x7FC00000.
+ *
+ * Moments in 8 bits (GB_STATE_E4M3): the codes and scales of m and of
+ * u = sqrt(v) are payloads of the fp8 codec (E4M3 codes, one float32 scale
+ * per 256 values, which gb_decode_sum decodes), with v = u * u.  After a step
+ * the block's scale is the smallest 2^e, e >= -126, with a <= 448 * 2^e for
+ * the block's largest finite magnitude a (1 for a = 0), and a value x becomes
+ * the code below or above x / 2^e: the 20 significand bits below the code's
+ * last (of a subnormal code: of the significand shifted to it) are added to
+ * 20 dither bits, and a carry rounds the magnitude up.  So a moment that a
+ * step moves by less than the distance of two codes still moves on average,
+ * and one that does not move keeps its code, since the grid stays where it
+ * is.  A root above 0 takes at least the code 1, so no update divides by eps
+ * alone; a value that is not finite takes the code 0x7F (NaN).  The update
+ * p' uses m' and v' before they are rounded.  All codes and scales zero is
+ * the state before the first step.
+ *   The dither: with G = 0x9E3779B97F4A7C15, z = seed + t * G (mod 2^64),
+ * three times z = (z ^ (z >> 32)) * G, key = z >> 32; with i the position of
+ * the value in the plan (each tensor starts at the next multiple of 256),
+ * x = (i / 2) * 0x9E3779B9 + key, x = (x ^ (x >> 15)) * 0x6A09E667,
+ * x = x ^ (x >> 16) (mod 2^32): the top 20 bits of x for even i, of
+ * x << 16 for odd i.  Both moments of a value use the same bits.
+ * ------------------------------------------------------------------------- */
+
+/* How a tensor's moments are held. */
+typedef enum gb_optim_state {
+  GB_STATE_F32 = 0, /* m and v float32                                        */
+  GB_STATE_E4M3 = 1 /* m and v: uint8 E4M3 codes of m and sqrt(v), with scales */
+} gb_optim_state;
+
+/* One tensor of a plan.  All pointers are device pointers; param, grad and
+ * copy need only the alignment of their element (they may be views into a
+ * bucket), m and v 16 bytes, the scales 4. */
+typedef struct gb_optim_tensor {
+  size_t n;           /* values; 0 leaves the tensor out (its pointers are not looked at) */
+  float* param;       /* read and written                                     */
+  const void* grad;   /* read; dtype                                          */
+  void* copy;         /* NULL, or n values of dtype, written: the model's low-precision parameters */
+  void* m;            /* read and written, as state says                      */
+  void* v;
+  float* m_scale;     /* GB_STATE_E4M3: ceil(n / 256) scales each; else NULL  */
+  float* v_scale;
+  int dtype;          /* GB_DTYPE_F32, F16 or BF16; a copy needs F16 or BF16  */
+  int state;          /* gb_optim_state                                       */
+  float lr_scale;     /* factor of the control block's lr (parameter groups)  */
+  float weight_decay; /* decoupled: p is scaled by 1 - lr_t * weight_decay    */
+} gb_optim_tensor;
+
+/* The control block: GB_OPTIM_CONTROL_BYTES of device memory, 16-byte
+ * aligned, zeroed by the caller before the first step, lr set by the caller
+ * (and written again by stream-ordered work whenever a schedule changes it).
+ * Resuming: set step to the number of steps taken. */
+#define GB_OPTIM_CONTROL_BYTES 64
+typedef struct gb_optim_control {
+  int64_t step;    /* steps taken, skipped ones not counted                   */
+  int64_t skipped; /* steps skipped because the norm was not finite           */
+  float lr;        /* learning rate                                           */
+  float norm;      /* gb_optim_begin_clip: the norm, times inv_scale          */
+  float coef;      /* factor the step applies to every gradient               */
+  int32_t skip;    /* 1: gb_adamw_step leaves everything as it is             */
+  float rate1;     /* 1 / (1 - beta1^t)                                       */
+  float rate2;     /* 1 / sqrt(1 - beta2^t)                                   */
+  uint32_t key;    /* dither key of the step                                  */
+  uint32_t reserved[3];
+} gb_optim_control;
+
+/* A plan's host part, filled by gb_optim_plan; copied freely, freed by
+ * nobody.  It refers to the workspace and to every buffer of the tensors,
+ * which must stay alive; a buffer that moved needs a new plan. */
+typedef struct gb_optim_handle {
+  uint64_t opaque[24];
+} gb_optim_handle;
+
+/* Largest number of tensors of a plan. */
+#define GB_OPTIM_MAX_TENSORS 65536
+
+/* Workspace bytes of a plan over tensors of ns[0..count) values; 0 for
+ * arguments gb_optim_plan would refuse.  Host only. */
+size_t gb_optim_plan_bytes(const size_t* ns, int count);
+
+/* Lays out `count` tensors (0 to GB_OPTIM_MAX_TENSORS; their sizes, each
+ * rounded up to a multiple of 256, add up to at most GB_MAX_N) for the step
+ * calls: validates them, fills *plan and enqueues small kernels that write
+ * the tables into the workspace (256-byte aligned device memory).  The host
+ * array may be reused when the call returns.  0 <= beta1, beta2 < 1;
+ * eps, rounded to binary32, above 0; lr_scale and weight_decay finite.
+ * Every buffer written (param, copy, m, v, scales, workspace) shares no byte
+ * with any other buffer of the plan.  One plan's calls belong on one stream
+ * at a time, or ordered by events: they share the workspace. */
+gb_status gb_optim_plan(gb_optim_handle* plan, const gb_optim_tensor* tensors, int count, double beta1,
+                        double beta2, double eps, uint64_t seed, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* Opens a step without a norm: step + 1, coef = RN32(inv_scale), skip = 0,
+ * the bias corrections and the dither key of the new step.  inv_scale: the
+ * reciprocal of a loss scale, or 1; finite and above 0. */
+gb_status gb_optim_begin(const gb_optim_handle* plan, void* control, double inv_scale, void* stream);
+
+/* Opens a step with the global gradient norm:
+ *   norm64 = inv_scale * sqrt(sum of g^2 over every value of every tensor)
+ *   norm = RN32(norm64)
+ *   coef = RN32(norm64 > max_norm ? inv_scale * max_norm / norm64 : inv_scale)
+ * Squares and sums are binary64 (a binary32 gradient's square neither
+ * overflows nor underflows there), added in an order fixed by the plan, so a
+ * result is bit-reproducible.  If norm is not finite (a gradient is Inf or
+ * NaN) the step is skipped: skip = 1, skipped + 1, coef 0, and step stays.
+ * max_norm above 0; INFINITY computes the norm and never clips.  One launch. */
+gb_status gb_optim_begin_clip(const gb_optim_handle* plan, void* control, double max_norm, double inv_scale,
+                              void* stream);
+
+/* The AdamW update of every tensor of the plan, for the step the last begin
+ * call on this control block opened.  One launch for each combination of
+ * gradient type and state that the plan holds. */
+gb_status gb_adamw_step(const gb_optim_handle* plan, const void* control, void* stream);
+
 /* Bytes one rank's n-value payload occupies on the bridge:
  * 4n (NONE), 2n (BF16), n + 4*ceil(n/256) (FP8).  0 for an unknown codec. */
 size_t gb_payload_bytes(int codec, size_t n);
