@@ -43,7 +43,7 @@ struct OptimChunk {
 };
 
 // Workgroups of the norm pass, and so partial sums, at most.
-constexpr uint32_t kNormGroups = 2048;
+constexpr uint32_t kNormGroups = 1024;
 
 // A plan's host part: what the handle's opaque words hold.
 struct OptimPlan {
@@ -51,9 +51,9 @@ struct OptimPlan {
   const OptimTensor* tensors;
   const OptimChunk* chunks;  // sorted by kind
   double* partials;
-  uint32_t* counter;  // 0 between calls
   double beta1, beta2;
   uint64_t seed;
+  size_t grad_bytes;  // of all gradients
   uint32_t first[kOptimKinds + 1];  // chunks [first[k], first[k + 1]) are of kind k
   float eps;
 };
@@ -68,9 +68,8 @@ struct OptimUpload {
 };
 static_assert(sizeof(OptimUpload) <= 3900, "an upload must fit the 4 KiB of kernel arguments");
 
-// Writes the upload's entries of both tables, and clears the counter.
-hipError_t launch_optim_upload(OptimTensor* tensors, OptimChunk* chunks, uint32_t* counter, const OptimUpload& up,
-                               hipStream_t stream);
+// Writes the upload's entries (one at least) of both tables.
+hipError_t launch_optim_upload(OptimTensor* tensors, OptimChunk* chunks, const OptimUpload& up, hipStream_t stream);
 hipError_t launch_optim_begin(const OptimPlan& plan, gb_optim_control* control, double inv_scale, hipStream_t stream);
 hipError_t launch_optim_begin_clip(const OptimPlan& plan, gb_optim_control* control, double max_norm,
                                    double inv_scale, hipStream_t stream);

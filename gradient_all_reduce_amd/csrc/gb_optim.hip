@@ -7,78 +7,138 @@
 namespace gb {
 namespace {
 
-// A wavefront's block of 256 values, 4 consecutive ones per lane.
+// A wavefront takes a block of 256 values, 4 consecutive ones per lane.
 constexpr int kWave = 64;
 constexpr int kWaves = kThreads / kWave;
-static_assert(kOptimChunk == (size_t)kThreads * 4, "a chunk is one vector per lane of a workgroup");
+// Up to this many chunks the norm is one launch of one workgroup.
+constexpr uint32_t kNormSmall = 64;
+// Up to this many bytes of gradients the norm pass reads them without the
+// non-temporal hint: the step that follows then finds them in the 256 MiB
+// last-level cache.  A clipped float32 step at 67, 134, 268, 537 MB of
+// gradients takes 85, 162, 324, 684 us with the hint left out and 91, 175,
+// 358, 710 us with it; at 4 GB the norm pass alone takes 648 and 581 us.
+constexpr size_t kNormKeepBytes = (size_t)640 << 20;
 
 // ---------------------------------------------------------------------------
-// Access at the alignment of the element: parameters, gradients and copies
-// may be views into a bucket that start at any value.
+// Access through the plan's pointers.  They come out of a table in memory, so
+// the compiler takes them for generic ones unless told otherwise: as global
+// pointers their loads and stores need no aperture check and no wait on the
+// LDS counter.  Parameters, gradients and copies may be views into a bucket
+// that start at any value, so theirs are aligned to the element only.
 // ---------------------------------------------------------------------------
+#define GB_GLOBAL __attribute__((address_space(1)))
 typedef f4 f4_any __attribute__((aligned(4)));
 typedef u2 u2_any __attribute__((aligned(2)));
+typedef uint16_t u16_any __attribute__((aligned(2)));
 
-template <bool FULL>
+template <class V, class T>
+__device__ __forceinline__ const GB_GLOBAL V* global_at(const T* p, size_t i) {
+  return (const GB_GLOBAL V*)(p + i);
+}
+template <class V, class T>
+__device__ __forceinline__ GB_GLOBAL V* global_at(T* p, size_t i) {
+  return (GB_GLOBAL V*)(p + i);
+}
+
+// KEEP: without the non-temporal hint, so that a later pass over the same
+// values finds them in the last-level cache.
+template <class V, bool KEEP>
+__device__ __forceinline__ V load_vec(const GB_GLOBAL V* p) {
+  if constexpr (KEEP) return *p;
+  else return __builtin_nontemporal_load(p);
+}
+
+// Values [i, i + 4), zero at and beyond n; V is f4, or f4_any where only the
+// element is aligned.
+template <class V, bool FULL, bool KEEP = false>
 __device__ __forceinline__ f4 load_f4(const float* p, size_t i, size_t n) {
-  if (FULL || i + 4 <= n) return __builtin_nontemporal_load(reinterpret_cast<const f4_any*>(p + i));
+  if (FULL || i + 4 <= n) return load_vec<V, KEEP>(global_at<V>(p, i));
   f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (i < n) v.x = p[i];
-  if (i + 1 < n) v.y = p[i + 1];
-  if (i + 2 < n) v.z = p[i + 2];
+  for (int e = 0; e < 3; e++) {
+    if (i + e < n) v[e] = *global_at<float>(p, i + e);
+  }
   return v;
 }
-template <bool FULL>
+template <class V, bool FULL>
 __device__ __forceinline__ void store_f4(float* p, size_t i, size_t n, f4 v) {
   if (FULL || i + 4 <= n) {
-    __builtin_nontemporal_store(v, reinterpret_cast<f4_any*>(p + i));
+    __builtin_nontemporal_store((V)v, global_at<V>(p, i));
     return;
   }
-  if (i < n) p[i] = v.x;
-  if (i + 1 < n) p[i + 1] = v.y;
-  if (i + 2 < n) p[i + 2] = v.z;
+  for (int e = 0; e < 3; e++) {
+    if (i + e < n) *global_at<float>(p, i + e) = v[e];
+  }
 }
-template <bool FULL>
-__device__ __forceinline__ u2 load_half4(const uint16_t* p, size_t i, size_t n) {
-  if (FULL || i + 4 <= n) return __builtin_nontemporal_load(reinterpret_cast<const u2_any*>(p + i));
+// Four 2-byte values as two words.
+template <bool FULL, bool KEEP = false>
+__device__ __forceinline__ u2 load_half4(const void* p, size_t i, size_t n) {
+  const uint16_t* h = static_cast<const uint16_t*>(p);
+  if (FULL || i + 4 <= n) return load_vec<u2_any, KEEP>(global_at<u2_any>(h, i));
   uint32_t w[2] = {0u, 0u};
   for (int e = 0; e < 3; e++) {
-    if (i + e < n) w[e >> 1] |= (uint32_t)p[i + e] << (16 * (e & 1));
+    if (i + e < n) w[e >> 1] |= (uint32_t)*global_at<uint16_t>(h, i + e) << (16 * (e & 1));
   }
   return u2{w[0], w[1]};
 }
 template <bool FULL>
-__device__ __forceinline__ void store_half4(uint16_t* p, size_t i, size_t n, u2 w) {
+__device__ __forceinline__ void store_half4(void* p, size_t i, size_t n, u2 w) {
+  uint16_t* h = static_cast<uint16_t*>(p);
   if (FULL || i + 4 <= n) {
-    __builtin_nontemporal_store(w, reinterpret_cast<u2_any*>(p + i));
+    __builtin_nontemporal_store((u2_any)w, global_at<u2_any>(h, i));
     return;
   }
   const uint32_t ws[2] = {w.x, w.y};
   for (int e = 0; e < 3; e++) {
-    if (i + e < n) p[i + e] = (uint16_t)(ws[e >> 1] >> (16 * (e & 1)));
+    if (i + e < n) *global_at<uint16_t>(h, i + e) = (uint16_t)(ws[e >> 1] >> (16 * (e & 1)));
+  }
+}
+// Four codes as a word (the arrays are 16-byte aligned, i a multiple of 4).
+template <bool FULL>
+__device__ __forceinline__ uint32_t load_codes(const void* p, size_t i, size_t n) {
+  const uint8_t* c = static_cast<const uint8_t*>(p);
+  if (FULL || i + 4 <= n) return __builtin_nontemporal_load(global_at<uint32_t>(c, i));
+  uint32_t w = 0;
+  for (int e = 0; e < 3; e++) {
+    if (i + e < n) w |= (uint32_t)*global_at<uint8_t>(c, i + e) << (8 * e);
+  }
+  return w;
+}
+template <bool FULL>
+__device__ __forceinline__ void store_codes(void* p, size_t i, size_t n, uint32_t w) {
+  uint8_t* c = static_cast<uint8_t*>(p);
+  if (FULL || i + 4 <= n) {
+    __builtin_nontemporal_store(w, global_at<uint32_t>(c, i));
+    return;
+  }
+  for (int e = 0; e < 3; e++) {
+    if (i + e < n) *global_at<uint8_t>(c, i + e) = (uint8_t)(w >> (8 * e));
   }
 }
 // Values [i, i + 4) of a gradient as binary32 (exact), zero at and beyond n.
-template <int ET, bool FULL>
+template <int ET, bool FULL, bool KEEP = false>
 __device__ __forceinline__ f4 load_grad4(const void* p, size_t i, size_t n) {
   if constexpr (ET == GB_DTYPE_F32) {
-    return load_f4<FULL>(static_cast<const float*>(p), i, n);
+    return load_f4<f4_any, FULL, KEEP>(static_cast<const float*>(p), i, n);
   } else {
-    const u2 w = load_half4<FULL>(static_cast<const uint16_t*>(p), i, n);
+    const u2 w = load_half4<FULL, KEEP>(p, i, n);
     if constexpr (ET == GB_DTYPE_BF16) return bf16_unpack4(w);
     const h4 h = __builtin_bit_cast(h4, w);
     return f4{(float)h.x, (float)h.y, (float)h.z, (float)h.w};
   }
 }
+// v, whose NaNs are canonical, rounded to a 2-byte type.
 template <int ET, bool FULL>
 __device__ __forceinline__ void store_copy4(void* p, size_t i, size_t n, f4 v) {
   static_assert(ET != GB_DTYPE_F32, "a copy is of a 2-byte type");
   if constexpr (ET == GB_DTYPE_BF16) {
-    store_half4<FULL>(static_cast<uint16_t*>(p), i, n, bf16_pack4(v));
+    // the converting instruction rounds to nearest even, two values at a
+    // time, where bf16_pack4 takes seven instructions a value
+    typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+    store_half4<FULL>(p, i, n, __builtin_bit_cast(u2, __builtin_convertvector(v, b4)));
   } else {
     asm volatile("" : "+v"(v));  // binary32 first, then its rounding to float16 (gb_device.h, store_vals4_at)
     const h4 h = {(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w};
-    store_half4<FULL>(static_cast<uint16_t*>(p), i, n, __builtin_bit_cast(u2, h));
+    store_half4<FULL>(p, i, n, __builtin_bit_cast(u2, h));
   }
 }
 
@@ -86,8 +146,7 @@ __device__ __forceinline__ void store_copy4(void* p, size_t i, size_t n, f4 v) {
 // The plan's tables
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kThreads) void optim_upload_kernel(OptimTensor* tensors, OptimChunk* chunks,
-                                                                uint32_t* counter, OptimUpload up) {
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *counter = 0;
+                                                                OptimUpload up) {
   const uint32_t i = blockIdx.x;
   if (i >= up.count) return;
   const uint32_t tensor = up.first_tensor + i;
@@ -143,58 +202,93 @@ __device__ void close_norm(gb_optim_control* c, const StepArgs& a, double sum) {
   open_step(c, a, (float)(norm > a.max_norm ? a.inv_scale * a.max_norm / norm : a.inv_scale));
 }
 
-// Sum over the workgroup, in an order fixed by the lane numbers; thread 0
-// holds it.
+// Sum over the workgroup, in an order fixed by the lane numbers; every thread
+// receives it.
+template <int WAVES>
 __device__ double group_sum(double s) {
-  __shared__ double part[kWaves];
+  __shared__ double part[WAVES];
   for (int d = kWave / 2; d > 0; d >>= 1) s += __shfl_xor(s, d);
-  __syncthreads();  // `part` may still be read from an earlier call
   if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = s;
   __syncthreads();
-  return (part[0] + part[1]) + (part[2] + part[3]);
+  double sum = part[0];
+#pragma unroll
+  for (int w = 1; w < WAVES; w++) sum += part[w];
+  return sum;
 }
 
-template <int ET>
-__device__ __forceinline__ double square4(const void* g, size_t i, size_t n, double s) {
-  const f4 x = i + 4 <= n ? load_grad4<ET, true>(g, i, n) : load_grad4<ET, false>(g, i, n);
+constexpr int kNormVecs = kOptimChunk / (4 * kWave);
+
+// Adds the squares of a chunk to s, the wavefront's lanes 4 values apart.
+// The product of two widened binary32 values is exact in binary64.
+template <int ET, bool FULL, bool KEEP>
+__device__ __forceinline__ double chunk_squares(const void* g, size_t i, size_t n, double s) {
+  f4 x[kNormVecs];
 #pragma unroll
-  for (int e = 0; e < 4; e++) s = fma((double)x[e], (double)x[e], s);  // the product is exact
+  for (int j = 0; j < kNormVecs; j++) x[j] = load_grad4<ET, FULL, KEEP>(g, i + j * 4 * kWave, n);
+#pragma unroll
+  for (int j = 0; j < kNormVecs; j++) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) s = fma((double)x[j][e], (double)x[j][e], s);
+  }
   return s;
 }
+template <int ET, bool KEEP>
+__device__ __forceinline__ double chunk_squares(const OptimTensor& t, uint32_t chunk, double s) {
+  const size_t first = (size_t)chunk * kOptimChunk, i = first + threadIdx.x % kWave * 4;
+  return first + kOptimChunk <= t.n ? chunk_squares<ET, true, KEEP>(t.g, i, t.n, s)
+                                    : chunk_squares<ET, false, KEEP>(t.g, i, t.n, s);
+}
 
-// Every workgroup sums the squares of its chunks (b, b + grid, ...) and
-// leaves one partial sum; the workgroup that counts last adds the partials
-// in order and opens the step.
-__global__ __launch_bounds__(kThreads) void optim_norm_kernel(const OptimTensor* tensors, const OptimChunk* chunks,
-                                                              uint32_t count, double* partials, uint32_t* counter,
-                                                              gb_optim_control* control, StepArgs a) {
+// The sum of the squares of chunks wave, wave + waves, ...: one chunk at a
+// time per wavefront, so that the tables are read as scalars and four loads
+// per lane are in flight; the next chunk's entry is read ahead.
+template <bool KEEP>
+__device__ __forceinline__ double wave_squares(const OptimTensor* tensors, const OptimChunk* chunks, uint32_t count,
+                                               uint32_t wave, uint32_t waves) {
   double s = 0.0;
-  for (uint32_t b = blockIdx.x; b < count; b += gridDim.x) {
-    const OptimChunk c = chunks[b];
-    const OptimTensor t = tensors[c.tensor];
-    const size_t i = (size_t)c.chunk * kOptimChunk + threadIdx.x * 4;
-    if (t.dtype == GB_DTYPE_F32) s = square4<GB_DTYPE_F32>(t.g, i, t.n, s);
-    else if (t.dtype == GB_DTYPE_F16) s = square4<GB_DTYPE_F16>(t.g, i, t.n, s);
-    else s = square4<GB_DTYPE_BF16>(t.g, i, t.n, s);
+  if (wave >= count) return s;
+  OptimChunk next = chunks[wave];
+  for (uint32_t b = wave; b < count; b += waves) {
+    const OptimChunk c = next;
+    if (b + waves < count) next = chunks[b + waves];
+    const OptimTensor& t = tensors[c.tensor];
+    if (t.dtype == GB_DTYPE_F32) s = chunk_squares<GB_DTYPE_F32, KEEP>(t, c.chunk, s);
+    else if (t.dtype == GB_DTYPE_F16) s = chunk_squares<GB_DTYPE_F16, KEEP>(t, c.chunk, s);
+    else s = chunk_squares<GB_DTYPE_BF16, KEEP>(t, c.chunk, s);
   }
-  s = group_sum(s);
-  __shared__ bool last;
-  if (threadIdx.x == 0) {
-    __hip_atomic_store(partials + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!last) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  double sum = 0.0;
-  for (uint32_t b = threadIdx.x; b < gridDim.x; b += kThreads) {
-    sum += __hip_atomic_load(partials + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  sum = group_sum(sum);
-  if (threadIdx.x == 0) {
-    *counter = 0;
-    close_norm(control, a, sum);
-  }
+  return s;
+}
+__device__ __forceinline__ uint32_t wave_in_group() {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+}
+
+// The norm in two launches: a partial sum per workgroup, then one workgroup
+// that adds them and opens the step.  (Counting the workgroups instead, so
+// that the last one adds, needs a release at device scope in each of them,
+// which on this chip writes the XCD's L2 back: 78 us instead of 16 for
+// 50 MB of gradients, and 19 us of that remain with relaxed atomics.)
+template <bool KEEP>
+__global__ __launch_bounds__(kThreads) void optim_norm_kernel(const OptimTensor* tensors, const OptimChunk* chunks,
+                                                              uint32_t count, double* partials) {
+  const double s = group_sum<kWaves>(
+      wave_squares<KEEP>(tensors, chunks, count, blockIdx.x * kWaves + wave_in_group(), gridDim.x * kWaves));
+  if (threadIdx.x == 0) partials[blockIdx.x] = s;
+}
+__global__ __launch_bounds__(kThreads) void optim_close_kernel(const double* partials, uint32_t count,
+                                                               gb_optim_control* control, StepArgs a) {
+  double s = 0.0;
+  for (uint32_t b = threadIdx.x; b < count; b += kThreads) s += partials[b];
+  s = group_sum<kWaves>(s);
+  if (threadIdx.x == 0) close_norm(control, a, s);
+}
+// Few chunks: one workgroup does both.
+constexpr int kSmallThreads = 1024;
+__global__ __launch_bounds__(kSmallThreads) void optim_norm_small_kernel(const OptimTensor* tensors,
+                                                                         const OptimChunk* chunks, uint32_t count,
+                                                                         gb_optim_control* control, StepArgs a) {
+  constexpr int waves = kSmallThreads / kWave;
+  const double s = group_sum<waves>(wave_squares<true>(tensors, chunks, count, wave_in_group(), waves));
+  if (threadIdx.x == 0) close_norm(control, a, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -222,67 +316,89 @@ __device__ __forceinline__ void adamw4(const AdamArgs& a, const Rates& r, f4 g, 
     v[e] = a.beta2 * v[e] + a.gain2 * (gs * gs);
     u[e] = __builtin_sqrtf(v[e]);
     const float d = u[e] * r.rate2 + a.eps;
-    p[e] = canon(p[e] * r.decay - r.step * (m[e] / d));
+    p[e] = p[e] * r.decay - r.step * (m[e] / d);
   }
 }
 
+// A step workgroup is one wavefront that takes 256 values, a quarter of a
+// chunk.  From one run on, consecutive workgroups take groups of 8 fronts
+// 1 MiB of float32 apart (GroupOrder in gb_device.h says why).
+// Chunks go to launches of at most kLaunchChunks, which keeps a launch's
+// lanes below 2^32.
+constexpr uint32_t kPerChunk = kOptimChunk / kBlock;
+constexpr uint32_t kLaunchChunks = 1u << 23;
+// The float32 step holds LDS it does not use, so that 16 workgroups share a
+// CU: 64-lane workgroups leave room for 32, and the fewer streams at once
+// gain 1.0-2.5% (67M bfloat16 values with a copy: 304 to 297 us; 1e9 float32
+// values: 4,560 to 4,510 us; 10 or 8 per CU lose again).  The 8-bit step is
+// bound by its arithmetic as well and wants every wavefront it can have (8%
+// slower with 20 per CU).
+constexpr unsigned kSixteenPerCuLds = 10u << 10;
+using StepOrder = GroupOrder<8, 1024, 1>;
+
+struct Piece {
+  OptimTensor t;  // a copy: the entry is read once, ahead of every store
+  size_t first;  // of 256 values
+};
+__device__ __forceinline__ Piece step_piece(const OptimTensor* tensors, const OptimChunk* chunks) {
+  const uint32_t w = (uint32_t)group_index<StepOrder>();
+  const OptimChunk c = chunks[w / kPerChunk];
+  return Piece{tensors[c.tensor], (size_t)c.chunk * kOptimChunk + w % kPerChunk * kBlock};
+}
+
 template <int ET, bool FULL>
-__device__ __forceinline__ void adamw_f32_chunk(const OptimTensor& t, const AdamArgs& a, const Rates& r, size_t i) {
+__device__ __forceinline__ void adamw_f32_piece(const OptimTensor& t, const AdamArgs& a, const Rates& r, size_t i) {
   const size_t n = t.n;
   const f4 g = load_grad4<ET, FULL>(t.g, i, n);
-  f4 p = load_f4<FULL>(t.p, i, n);
-  f4 m = load4_at<FULL>(static_cast<const float*>(t.m), i, n);
-  f4 v = load4_at<FULL>(static_cast<const float*>(t.v), i, n);
+  f4 p = load_f4<f4_any, FULL>(t.p, i, n);
+  f4 m = load_f4<f4, FULL>(static_cast<const float*>(t.m), i, n);
+  f4 v = load_f4<f4, FULL>(static_cast<const float*>(t.v), i, n);
   f4 u;
   adamw4(a, r, g, p, m, v, u);
-  store_f4<FULL>(t.p, i, n, p);
-  store4_at<FULL>(static_cast<float*>(t.m), i, n, canon4(m));
-  store4_at<FULL>(static_cast<float*>(t.v), i, n, canon4(v));
+  p = canon4(p);
+  store_f4<f4_any, FULL>(t.p, i, n, p);
+  store_f4<f4, FULL>(static_cast<float*>(t.m), i, n, canon4(m));
+  store_f4<f4, FULL>(static_cast<float*>(t.v), i, n, canon4(v));
   if constexpr (ET != GB_DTYPE_F32) {
     if (t.copy != nullptr) store_copy4<ET, FULL>(t.copy, i, n, p);
   }
 }
 
 template <int ET>
-__global__ __launch_bounds__(kThreads) void adamw_f32_kernel(const OptimTensor* tensors, const OptimChunk* chunks,
-                                                             const gb_optim_control* control, AdamArgs a) {
+__global__ __launch_bounds__(kWave) void adamw_f32_kernel(const OptimTensor* tensors, const OptimChunk* chunks,
+                                                          const gb_optim_control* control, AdamArgs a) {
   if (control->skip != 0) return;
-  const OptimChunk c = chunks[blockIdx.x];
-  const OptimTensor t = tensors[c.tensor];
-  const Rates r = tensor_rates(control, t);
-  const size_t first = (size_t)c.chunk * kOptimChunk, i = first + threadIdx.x * 4;
-  if (first + kOptimChunk <= t.n) adamw_f32_chunk<ET, true>(t, a, r, i);
-  else adamw_f32_chunk<ET, false>(t, a, r, i);
+  const Piece w = step_piece(tensors, chunks);
+  if (w.first >= w.t.n) return;
+  const Rates r = tensor_rates(control, w.t);
+  const size_t i = w.first + threadIdx.x * 4;
+  if (w.first + kBlock <= w.t.n) adamw_f32_piece<ET, true>(w.t, a, r, i);
+  else adamw_f32_piece<ET, false>(w.t, a, r, i);
 }
 
-// The largest finite magnitude of the wavefront's values, as a bit pattern,
-// the same in every lane; the values that are not finite count as 0.
+// The largest magnitude of the wavefront's values, as a bit pattern; NaN
+// counts as 0 (the maximum instruction passes over it).
 __device__ __forceinline__ uint32_t wave_absmax(f4 x) {
-  uint32_t b[4], top = 0u;
-#pragma unroll
-  for (int e = 0; e < 4; e++) {
-    b[e] = fbits(x[e]) & 0x7FFFFFFFu;
-    top = max(top, b[e]);
-  }
-  if (top >= 0x7F800000u) {
-    top = 0u;
-#pragma unroll
-    for (int e = 0; e < 4; e++) top = max(top, b[e] >= 0x7F800000u ? 0u : b[e]);
-  }
-  top = row_max16(top);
+  const float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+  const uint32_t top = row_max16(a == a ? fbits(a) : 0u);
   const uint32_t r0 = (uint32_t)__builtin_amdgcn_readlane((int)top, 0);
   const uint32_t r1 = (uint32_t)__builtin_amdgcn_readlane((int)top, 16);
   const uint32_t r2 = (uint32_t)__builtin_amdgcn_readlane((int)top, 32);
   const uint32_t r3 = (uint32_t)__builtin_amdgcn_readlane((int)top, 48);
   return max(max(r0, r1), max(r2, r3));
 }
+// The same over the finite values only: x with 0 for the others.
+__device__ __forceinline__ f4 finite4(f4 x) {
+#pragma unroll
+  for (int e = 0; e < 4; e++) x[e] = fabsf(x[e]) < __builtin_inff() ? x[e] : 0.0f;
+  return x;
+}
 
 // Exponent e of a block's scale 2^e: the smallest, at least -126, with
 // a <= 448 * 2^e = 1.75 * 2^(e + 8); 0 for a = 0.  A finite a gives e <= 120.
 __device__ __forceinline__ int scale_exponent(uint32_t abits) {
   if (abits == 0u) return 0;
-  const int e = (int)(abits >> 23) - 127 - 8 + ((abits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return max(e, -126);
+  return max((int)((abits + 0x1FFFFFu) >> 23) - 135, -126);  // the sum carries where the fraction exceeds 0.75
 }
 __device__ __forceinline__ float pow2(int e) { return bitsf((uint32_t)(e + 127) << 23); }
 
@@ -303,7 +419,7 @@ __device__ __forceinline__ uint32_t dithered4(f4 q, const uint32_t (&seed)[4]) {
 __device__ __forceinline__ uint32_t mark_not_finite(f4 x, uint32_t w) {
 #pragma unroll
   for (int e = 0; e < 4; e++) {
-    if ((fbits(x[e]) & 0x7FFFFFFFu) >= 0x7F800000u) w = (w & ~(0xFFu << (8 * e))) | (0x7Fu << (8 * e));
+    if (!(fabsf(x[e]) < __builtin_inff())) w = (w & ~(0xFFu << (8 * e))) | (0x7Fu << (8 * e));
   }
   return w;
 }
@@ -315,50 +431,70 @@ __device__ __forceinline__ uint32_t dither_word(uint32_t x) {
 
 template <int ET, bool FULL>
 __device__ __forceinline__ void adamw_e4m3_block(const OptimTensor& t, const AdamArgs& a, const Rates& r,
-                                                 uint32_t key, size_t block, size_t i) {
-  const size_t n = t.n;
-  uint8_t* mc = static_cast<uint8_t*>(t.m);
-  uint8_t* vc = static_cast<uint8_t*>(t.v);
+                                                 uint32_t key, size_t first) {
+  const size_t n = t.n, block = first / kBlock, i = first + threadIdx.x * 4;
   const f4 g = load_grad4<ET, FULL>(t.g, i, n);
-  f4 p = load_f4<FULL>(t.p, i, n);
-  const uint32_t mw = load_codes4_at<FULL>(mc, i, n), vw = load_codes4_at<FULL>(vc, i, n);
-  f4 m = e4m3_unpack4(mw) * t.ms[block];
-  f4 u = e4m3_unpack4(vw) * t.vs[block];
+  f4 p = load_f4<f4_any, FULL>(t.p, i, n);
+  const uint32_t mw = load_codes<FULL>(t.m, i, n), vw = load_codes<FULL>(t.v, i, n);
+  // The scales come as vector loads although their address is the same in
+  // every lane: 4 bytes a block through the scalar cache made the step 6%
+  // slower.  The empty asm keeps the address in vector registers.
+  size_t at = block;
+  asm("" : "+v"(at));
+  f4 m = e4m3_unpack4(mw) * *global_at<float>(t.ms, at);
+  f4 u = e4m3_unpack4(vw) * *global_at<float>(t.vs, at);
   f4 v = u * u;
   adamw4(a, r, g, p, m, v, u);
-  store_f4<FULL>(t.p, i, n, p);
+
+  // What is not finite is rare and handled for the wavefront as a whole: a
+  // NaN in m' or u reaches p', an infinity shows in the largest magnitude.
+  uint32_t mtop = wave_absmax(m), utop = wave_absmax(u);
+  const bool nan = __builtin_isunordered(p.x, p.y) || __builtin_isunordered(p.z, p.w);
+  const bool special = mtop >= 0x7F800000u || utop >= 0x7F800000u || __any(nan);
+  if (special) {
+    p = canon4(p);
+    mtop = wave_absmax(finite4(m));
+    utop = wave_absmax(finite4(u));
+  }
+  store_f4<f4_any, FULL>(t.p, i, n, p);
   if constexpr (ET != GB_DTYPE_F32) {
     if (t.copy != nullptr) store_copy4<ET, FULL>(t.copy, i, n, p);
   }
-  const int me = scale_exponent(wave_absmax(m)), ue = scale_exponent(wave_absmax(u));
+
+  const int me = scale_exponent(mtop), ue = scale_exponent(utop);
   const f4 mq = m * pow2(-me);
   f4 uq = u * pow2(-ue);
+  // a root above 0 keeps a code: at least the smallest, 2^-9
+  if (__any(fminf(fminf(uq.x, uq.y), fminf(uq.z, uq.w)) < 0x1p-9f)) {
 #pragma unroll
-  for (int e = 0; e < 4; e++) uq[e] = u[e] > 0.0f ? fmaxf(uq[e], 0x1p-9f) : uq[e];  // a root above 0 keeps a code
-  const uint32_t pair = (t.first_block * 128u) + (uint32_t)(i / 2);
-  const uint32_t x0 = dither_word(pair * 0x9E3779B9u + key), x1 = dither_word((pair + 1) * 0x9E3779B9u + key);
+    for (int e = 0; e < 4; e++) uq[e] = u[e] > 0.0f ? fmaxf(uq[e], 0x1p-9f) : uq[e];
+  }
+  const uint32_t base = (t.first_block * 128u + (uint32_t)(first / 2)) * 0x9E3779B9u + key;  // of the block's first pair
+  const uint32_t x = base + threadIdx.x * (2 * 0x9E3779B9u);
+  const uint32_t x0 = dither_word(x), x1 = dither_word(x + 0x9E3779B9u);
   const uint32_t seed[4] = {x0, x0 << 16, x1, x1 << 16};
-  store_codes4_at<FULL>(mc, i, n, mark_not_finite(m, dithered4(mq, seed)));
-  store_codes4_at<FULL>(vc, i, n, mark_not_finite(u, dithered4(uq, seed)));
-  if (threadIdx.x % kWave == 0) {
-    t.ms[block] = pow2(me);
-    t.vs[block] = pow2(ue);
+  uint32_t mc = dithered4(mq, seed), uc = dithered4(uq, seed);
+  if (special) {
+    mc = mark_not_finite(m, mc);
+    uc = mark_not_finite(u, uc);
+  }
+  store_codes<FULL>(t.m, i, n, mc);
+  store_codes<FULL>(t.v, i, n, uc);
+  if (threadIdx.x == 0) {
+    *global_at<float>(t.ms, block) = pow2(me);
+    *global_at<float>(t.vs, block) = pow2(ue);
   }
 }
 
 template <int ET>
-__global__ __launch_bounds__(kThreads) void adamw_e4m3_kernel(const OptimTensor* tensors, const OptimChunk* chunks,
-                                                              const gb_optim_control* control, AdamArgs a) {
+__global__ __launch_bounds__(kWave) void adamw_e4m3_kernel(const OptimTensor* tensors, const OptimChunk* chunks,
+                                                           const gb_optim_control* control, AdamArgs a) {
   if (control->skip != 0) return;
-  const OptimChunk c = chunks[blockIdx.x];
-  const OptimTensor t = tensors[c.tensor];
-  const Rates r = tensor_rates(control, t);
-  const size_t first = (size_t)c.chunk * kOptimChunk, i = first + threadIdx.x * 4;
-  // one block per wavefront: the last chunk's wavefronts beyond n leave whole
-  const size_t block = first / kBlock + threadIdx.x / kWave;
-  if (block * kBlock >= t.n) return;
-  if (first + kOptimChunk <= t.n) adamw_e4m3_block<ET, true>(t, a, r, control->key, block, i);
-  else adamw_e4m3_block<ET, false>(t, a, r, control->key, block, i);
+  const Piece w = step_piece(tensors, chunks);
+  if (w.first >= w.t.n) return;
+  const Rates r = tensor_rates(control, w.t);
+  if (w.first + kBlock <= w.t.n) adamw_e4m3_block<ET, true>(w.t, a, r, control->key, w.first);
+  else adamw_e4m3_block<ET, false>(w.t, a, r, control->key, w.first);
 }
 
 StepArgs step_args(const OptimPlan& plan, double max_norm, double inv_scale) {
@@ -367,10 +503,9 @@ StepArgs step_args(const OptimPlan& plan, double max_norm, double inv_scale) {
 
 }  // namespace
 
-hipError_t launch_optim_upload(OptimTensor* tensors, OptimChunk* chunks, uint32_t* counter, const OptimUpload& up,
-                               hipStream_t stream) {
+hipError_t launch_optim_upload(OptimTensor* tensors, OptimChunk* chunks, const OptimUpload& up, hipStream_t stream) {
   (void)hipGetLastError();
-  optim_upload_kernel<<<dim3(up.count > 0 ? up.count : 1, 8), kThreads, 0, stream>>>(tensors, chunks, counter, up);
+  optim_upload_kernel<<<dim3(up.count, 8), kThreads, 0, stream>>>(tensors, chunks, up);
   return hipGetLastError();
 }
 
@@ -384,10 +519,18 @@ hipError_t launch_optim_begin(const OptimPlan& plan, gb_optim_control* control, 
 hipError_t launch_optim_begin_clip(const OptimPlan& plan, gb_optim_control* control, double max_norm,
                                    double inv_scale, hipStream_t stream) {
   const uint32_t count = plan.first[kOptimKinds];
-  const uint32_t groups = count < 1 ? 1 : count < kNormGroups ? count : kNormGroups;
+  const StepArgs a = step_args(plan, max_norm, inv_scale);
   (void)hipGetLastError();
-  optim_norm_kernel<<<groups, kThreads, 0, stream>>>(plan.tensors, plan.chunks, count, plan.partials, plan.counter,
-                                                     control, step_args(plan, max_norm, inv_scale));
+  if (count <= kNormSmall) {
+    optim_norm_small_kernel<<<1, kSmallThreads, 0, stream>>>(plan.tensors, plan.chunks, count, control, a);
+    return hipGetLastError();
+  }
+  const uint32_t groups = (count + kWaves - 1) / kWaves < kNormGroups ? (count + kWaves - 1) / kWaves : kNormGroups;
+  const auto kernel = plan.grad_bytes <= kNormKeepBytes ? optim_norm_kernel<true> : optim_norm_kernel<false>;
+  kernel<<<groups, kThreads, 0, stream>>>(plan.tensors, plan.chunks, count, plan.partials);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  optim_close_kernel<<<1, kThreads, 0, stream>>>(plan.partials, groups, control, a);
   return hipGetLastError();
 }
 
@@ -400,11 +543,13 @@ hipError_t launch_adamw(const OptimPlan& plan, const gb_optim_control* control, 
                       plan.eps};
   (void)hipGetLastError();
   for (int k = 0; k < kOptimKinds; k++) {
-    const uint32_t count = plan.first[k + 1] - plan.first[k];
-    if (count == 0) continue;
-    kernels[k]<<<count, kThreads, 0, stream>>>(plan.tensors, plan.chunks + plan.first[k], control, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    for (uint32_t c = plan.first[k]; c < plan.first[k + 1]; c += kLaunchChunks) {
+      const uint32_t left = plan.first[k + 1] - c, count = left < kLaunchChunks ? left : kLaunchChunks;
+      kernels[k]<<<count * kPerChunk, kWave, k < 3 ? kSixteenPerCuLds : 0, stream>>>(plan.tensors, plan.chunks + c,
+                                                                                     control, a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
   return hipSuccess;
 }

@@ -37,16 +37,15 @@ size_t nblocks(size_t n) { return (n + GB_BLOCK - 1) / GB_BLOCK; }
 size_t nchunks(size_t n) { return (n + gb::kOptimChunk - 1) / gb::kOptimChunk; }
 size_t elem_size(int dtype) { return dtype == GB_DTYPE_F32 ? 4 : 2; }
 
-// Byte offsets in a plan's workspace: tensors, chunks, partial sums, counter.
+// Byte offsets in a plan's workspace: tensors, chunks, partial sums.
 struct Layout {
-  size_t chunks, partials, counter, total;
+  size_t chunks, partials, total;
 };
 Layout layout(size_t count, size_t chunks) {
   Layout l;
   l.chunks = round_up(count * sizeof(gb::OptimTensor), kWorkspaceAlign);
   l.partials = l.chunks + round_up(chunks * sizeof(gb::OptimChunk), kWorkspaceAlign);
-  l.counter = l.partials + gb::kNormGroups * sizeof(double);
-  l.total = l.counter + kWorkspaceAlign;
+  l.total = l.partials + gb::kNormGroups * sizeof(double);
   return l;
 }
 
@@ -166,13 +165,13 @@ gb_status make_plan(const char* fn, gb_optim_handle* handle, const gb_optim_tens
   plan.tensors = table;
   plan.chunks = map;
   plan.partials = reinterpret_cast<double*>(ws + l.partials);
-  plan.counter = reinterpret_cast<uint32_t*>(ws + l.counter);
   plan.beta1 = beta1;
   plan.beta2 = beta2;
   plan.seed = seed;
   plan.eps = (float)eps;
   for (int i = 0; i < count; i++) {
     if (tensors[i].n == 0) continue;
+    plan.grad_bytes += elem_size(tensors[i].dtype) * tensors[i].n;
     plan.first[gb::optim_kind(tensors[i].dtype, tensors[i].state) + 1] += (uint32_t)nchunks(tensors[i].n);
   }
   for (int k = 0; k < gb::kOptimKinds; k++) plan.first[k + 1] += plan.first[k];
@@ -183,7 +182,7 @@ gb_status make_plan(const char* fn, gb_optim_handle* handle, const gb_optim_tens
   hipError_t e = hipSuccess;
   gb::OptimUpload up = {};
   auto flush = [&]() {
-    if (e == hipSuccess) e = gb::launch_optim_upload(table, map, plan.counter, up, stream);
+    if (e == hipSuccess) e = gb::launch_optim_upload(table, map, up, stream);
     up.first_tensor += up.count;
     up.count = 0;
   };
@@ -201,7 +200,7 @@ gb_status make_plan(const char* fn, gb_optim_handle* handle, const gb_optim_tens
     up.t[up.count++] = d;
     if (up.count == gb::kOptimUpload) flush();
   }
-  if (up.count > 0 || count == 0) flush();
+  if (up.count > 0) flush();
   if (e != hipSuccess) return from_hip(e, fn);
   std::memset(handle, 0, sizeof *handle);
   std::memcpy(handle, &plan, sizeof plan);

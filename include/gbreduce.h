@@ -716,13 +716,13 @@ gb_status gb_optim_begin(const gb_optim_handle* plan, void* control, double inv_
  * overflows nor underflows there), added in an order fixed by the plan, so a
  * result is bit-reproducible.  If norm is not finite (a gradient is Inf or
  * NaN) the step is skipped: skip = 1, skipped + 1, coef 0, and step stays.
- * max_norm above 0; INFINITY computes the norm and never clips.  One launch. */
+ * max_norm above 0; INFINITY computes the norm and never clips.  One or two launches. */
 gb_status gb_optim_begin_clip(const gb_optim_handle* plan, void* control, double max_norm, double inv_scale,
                               void* stream);
 
 /* The AdamW update of every tensor of the plan, for the step the last begin
  * call on this control block opened.  One launch for each combination of
- * gradient type and state that the plan holds. */
+ * gradient type and state that the plan holds (and for each 2^33 values). */
 gb_status gb_adamw_step(const gb_optim_handle* plan, const void* control, void* stream);
 
 /* Bytes one rank's n-value payload occupies on the bridge:

@@ -387,10 +387,12 @@ def test_runs_repeat_bit_for_bit(gb):
     assert len(got) == 1
 
 
-def test_a_tensor_beyond_32_bit_offsets(gb):
-    """2^32 + 517 values: the last ones are updated as the oracle says, the
-    dither counting from their position."""
-    n = (1 << 32) + 517
+@pytest.mark.parametrize("bits", [32, 33])
+def test_a_tensor_beyond_32_bit_offsets(gb, bits):
+    """2^32 + 517 values, and 2^33 + 517, which take a second launch: the
+    last ones are updated as the oracle says, the dither counting from their
+    position."""
+    n = (1 << bits) + 517
     tail = 517 + 256 * 5
     p = torch.zeros(n, device=DEV)
     g = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
