@@ -575,11 +575,11 @@ class GbOptimPlan:
     """A list of tensors laid out for gb_optim_begin, gb_optim_begin_clip and
     gb_adamw_step; made by gb_optim_plan, keeps its tensors and workspace."""
 
-    __slots__ = ("handle", "ref", "tensors", "workspace", "device")
+    __slots__ = ("handle", "ref", "tensors", "workspace", "device_index")
 
     def __init__(self, handle, tensors, workspace):
         self.handle, self.tensors, self.workspace = handle, tensors, workspace
-        self.ref, self.device = ctypes.byref(handle), workspace.device
+        self.ref, self.device_index = ctypes.byref(handle), workspace.device.index
 
 
 def gb_optim_plan_bytes(ns):
@@ -587,30 +587,36 @@ def gb_optim_plan_bytes(ns):
     return int(_lib.gb_optim_plan_bytes(_size_array(ns), len(ns)))
 
 
-def _optim_entry(i, t):
-    n = t.param.numel() if isinstance(t.param, torch.Tensor) else 0
-    name = f"tensors[{i}]"
-    _device_tensor(t.param, torch.float32, name + ".param")
-    if not isinstance(t.grad, torch.Tensor) or t.grad.dtype not in (torch.float32, torch.float16, torch.bfloat16):
-        raise TypeError(f"{name}.grad must be a tensor of float32, float16 or bfloat16")
-    _device_tensor(t.grad, t.grad.dtype, name + ".grad")
-    coded = isinstance(t.m, torch.Tensor) and t.m.dtype == torch.uint8
-    for part, dtype in (("m", torch.uint8 if coded else torch.float32), ("v", torch.uint8 if coded else torch.float32)):
-        _device_tensor(getattr(t, part), dtype, f"{name}.{part}")
-        _same_numel([getattr(t, part)], n, f"{name}.{part}")
-    _same_numel([t.grad], n, name + ".grad")
-    for part in ("m_scale", "v_scale"):
-        scale = getattr(t, part)
-        if coded:
-            _device_tensor(scale, torch.float32, f"{name}.{part}")
-            _same_numel([scale], (n + GB_BLOCK - 1) // GB_BLOCK, f"{name}.{part}")
-    if t.copy is not None:
-        _device_tensor(t.copy, t.grad.dtype, name + ".copy")
-        _same_numel([t.copy], n, name + ".copy")
-    ptr = lambda x: x.data_ptr() if x is not None else None  # noqa: E731
-    return _OptimTensor(n, ptr(t.param), ptr(t.grad), ptr(t.copy), ptr(t.m), ptr(t.v), ptr(t.m_scale), ptr(t.v_scale),
-                        GB_DTYPE[t.grad.dtype], GB_STATE_E4M3 if coded else GB_STATE_F32, float(t.lr_scale),
-                        float(t.weight_decay))
+_OPTIM_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _optim_part(x, dtype, n, device, i, part):
+    """Address of one buffer of tensors[i], checked."""
+    if not (isinstance(x, torch.Tensor) and x.dtype is dtype and x.is_cuda and x.device == device
+            and x.is_contiguous() and x.numel() == n):
+        name = f"tensors[{i}].{part}"
+        _device_tensor(x, dtype, name)
+        if x.device != device:
+            raise ValueError(f"{name} is on {x.device}, the workspace on {device}")
+        raise ValueError(f"{name} has {x.numel()} elements, expected {n}")
+    return x.data_ptr()
+
+
+def _optim_entry(i, t, device):
+    param, grad, m, v, m_scale, v_scale, copy, lr_scale, weight_decay = t
+    _optim_part(param, torch.float32, n := param.numel() if isinstance(param, torch.Tensor) else 0, device, i, "param")
+    if not isinstance(grad, torch.Tensor) or grad.dtype not in _OPTIM_TYPES:
+        raise TypeError(f"tensors[{i}].grad must be a tensor of one of {list(_OPTIM_TYPES)}")
+    coded = isinstance(m, torch.Tensor) and m.dtype is torch.uint8
+    moment = torch.uint8 if coded else torch.float32
+    blocks = (n + GB_BLOCK - 1) // GB_BLOCK
+    # scales of float32 moments are the library's to refuse
+    scales = [_optim_part(x, torch.float32, blocks if coded else x.numel(), device, i, part) if coded or x is not None
+              else None for x, part in ((m_scale, "m_scale"), (v_scale, "v_scale"))]
+    return (n, param.data_ptr(), _optim_part(grad, grad.dtype, n, device, i, "grad"),
+            None if copy is None else _optim_part(copy, grad.dtype, n, device, i, "copy"),
+            _optim_part(m, moment, n, device, i, "m"), _optim_part(v, moment, n, device, i, "v"), *scales,
+            _OPTIM_TYPES[grad.dtype], GB_STATE_E4M3 if coded else GB_STATE_F32, lr_scale, weight_decay)
 
 
 def gb_optim_plan(tensors, workspace, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, stream=None):
@@ -618,13 +624,9 @@ def gb_optim_plan(tensors, workspace, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, 
     of gb_optim_plan_bytes([t.param.numel() for t in tensors]) bytes, and seed
     that of the 8-bit moments' dither.  Returns the GbOptimPlan."""
     tensors = list(tensors)
-    table = (_OptimTensor * max(1, len(tensors)))(*[_optim_entry(i, t) for i, t in enumerate(tensors)])
+    device = workspace.device if isinstance(workspace, torch.Tensor) else None
+    table = (_OptimTensor * max(1, len(tensors)))(*[_optim_entry(i, t, device) for i, t in enumerate(tensors)])
     _device_tensor(workspace, torch.uint8, "workspace")
-    for i, t in enumerate(tensors):
-        for part in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy"):
-            x = getattr(t, part)
-            if x is not None and x.device != workspace.device:
-                raise ValueError(f"tensors[{i}].{part} is on {x.device}, the workspace on {workspace.device}")
     handle = _OptimHandle()
     _check(_lib.gb_optim_plan(ctypes.byref(handle), table, len(tensors), float(beta1), float(beta2), float(eps),
                               int(seed) & 0xFFFFFFFFFFFFFFFF, *_workspace_args(workspace),
@@ -633,10 +635,23 @@ def gb_optim_plan(tensors, workspace, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, 
 
 
 def _control(control):
+    """Address of a control block."""
+    try:
+        if (control.dtype is torch.uint8 and control.is_cuda and control.numel() == GB_OPTIM_CONTROL_BYTES
+                and control.is_contiguous()):
+            return control.data_ptr()
+    except AttributeError:
+        pass
     _device_tensor(control, torch.uint8, "control")
-    if control.numel() != GB_OPTIM_CONTROL_BYTES:
-        raise ValueError(f"control has {control.numel()} bytes, expected {GB_OPTIM_CONTROL_BYTES}")
-    return ctypes.c_void_p(control.data_ptr())
+    raise ValueError(f"control has {control.numel()} bytes, expected {GB_OPTIM_CONTROL_BYTES}")
+
+
+def _plan_stream(plan, stream):
+    """Handle of the stream, or of the plan's device's current one: read
+    without making a Stream object, which takes as long as half a launch."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(plan.device_index)
 
 
 def gb_optim_control(control):
@@ -653,18 +668,19 @@ def gb_optim_control(control):
 
 def gb_optim_begin(plan, control, inv_scale=1.0, stream=None):
     """Open a step: the gradients are scaled by inv_scale (1 / loss scale)."""
-    _check(_lib.gb_optim_begin(plan.ref, _control(control), inv_scale, _stream(stream, plan.device)))
+    _check(_lib.gb_optim_begin(plan.ref, _control(control), inv_scale, _plan_stream(plan, stream)))
 
 
 def gb_optim_begin_clip(plan, control, max_norm, inv_scale=1.0, stream=None):
     """Open a step with the global gradient norm, clipped to max_norm; a norm
     that is not finite skips the step."""
-    _check(_lib.gb_optim_begin_clip(plan.ref, _control(control), max_norm, inv_scale, _stream(stream, plan.device)))
+    _check(_lib.gb_optim_begin_clip(plan.ref, _control(control), max_norm, inv_scale,
+                                    _plan_stream(plan, stream)))
 
 
 def gb_adamw_step(plan, control, stream=None):
     """The AdamW update of every tensor of the plan, for the step last opened."""
-    _check(_lib.gb_adamw_step(plan.ref, _control(control), _stream(stream, plan.device)))
+    _check(_lib.gb_adamw_step(plan.ref, _control(control), _plan_stream(plan, stream)))
 
 
 def gb_payload_bytes(codec, n):

@@ -175,22 +175,34 @@ __device__ double power(double b, int64_t t) {
   return r;
 }
 
-__device__ void open_step(gb_optim_control* c, const StepArgs& a, float coef) {
+// What the next step's number alone decides.
+struct Opening {
+  int64_t step;
+  float rate1, rate2;
+  uint32_t key;
+};
+__device__ Opening next_step(const gb_optim_control* c, const StepArgs& a) {
   const int64_t t = c->step + 1;
-  c->step = t;
-  c->skip = 0;
-  c->coef = coef;
-  c->rate1 = (float)(1.0 / (1.0 - power(a.beta1, t)));
-  c->rate2 = (float)(1.0 / sqrt(1.0 - power(a.beta2, t)));
   constexpr uint64_t kGolden = 0x9E3779B97F4A7C15ull;
   uint64_t z = a.seed + (uint64_t)t * kGolden;
   for (int i = 0; i < 3; i++) z = (z ^ (z >> 32)) * kGolden;
-  c->key = (uint32_t)(z >> 32);
+  return Opening{t, (float)(1.0 / (1.0 - power(a.beta1, t))), (float)(1.0 / sqrt(1.0 - power(a.beta2, t))),
+                 (uint32_t)(z >> 32)};
+}
+__device__ void open_step(gb_optim_control* c, const Opening& o, float coef) {
+  c->step = o.step;
+  c->skip = 0;
+  c->coef = coef;
+  c->rate1 = o.rate1;
+  c->rate2 = o.rate2;
+  c->key = o.key;
 }
 
-__global__ void optim_begin_kernel(gb_optim_control* c, StepArgs a) { open_step(c, a, (float)a.inv_scale); }
+__global__ void optim_begin_kernel(gb_optim_control* c, StepArgs a) {
+  open_step(c, next_step(c, a), (float)a.inv_scale);
+}
 
-__device__ void close_norm(gb_optim_control* c, const StepArgs& a, double sum) {
+__device__ void close_norm(gb_optim_control* c, const StepArgs& a, const Opening& o, double sum) {
   const double norm = a.inv_scale * sqrt(sum);
   c->norm = (float)norm;
   if (!(fabsf((float)norm) < __builtin_inff())) {
@@ -199,7 +211,7 @@ __device__ void close_norm(gb_optim_control* c, const StepArgs& a, double sum) {
     c->skipped += 1;
     return;
   }
-  open_step(c, a, (float)(norm > a.max_norm ? a.inv_scale * a.max_norm / norm : a.inv_scale));
+  open_step(c, o, (float)(norm > a.max_norm ? a.inv_scale * a.max_norm / norm : a.inv_scale));
 }
 
 // Sum over the workgroup, in an order fixed by the lane numbers; every thread
@@ -274,12 +286,16 @@ __global__ __launch_bounds__(kThreads) void optim_norm_kernel(const OptimTensor*
       wave_squares<KEEP>(tensors, chunks, count, blockIdx.x * kWaves + wave_in_group(), gridDim.x * kWaves));
   if (threadIdx.x == 0) partials[blockIdx.x] = s;
 }
+// The last thread works out the new step's rates meanwhile: the powers are a
+// chain of some 20 binary64 products and two divisions, about 1 us.
 __global__ __launch_bounds__(kThreads) void optim_close_kernel(const double* partials, uint32_t count,
                                                                gb_optim_control* control, StepArgs a) {
+  __shared__ Opening opening;
   double s = 0.0;
   for (uint32_t b = threadIdx.x; b < count; b += kThreads) s += partials[b];
+  if (threadIdx.x == kThreads - 1) opening = next_step(control, a);
   s = group_sum<kWaves>(s);
-  if (threadIdx.x == 0) close_norm(control, a, s);
+  if (threadIdx.x == 0) close_norm(control, a, opening, s);
 }
 // Few chunks: one workgroup does both.
 constexpr int kSmallThreads = 1024;
@@ -287,8 +303,10 @@ __global__ __launch_bounds__(kSmallThreads) void optim_norm_small_kernel(const O
                                                                          const OptimChunk* chunks, uint32_t count,
                                                                          gb_optim_control* control, StepArgs a) {
   constexpr int waves = kSmallThreads / kWave;
+  __shared__ Opening opening;
+  if (threadIdx.x == kSmallThreads - 1) opening = next_step(control, a);
   const double s = group_sum<waves>(wave_squares<true>(tensors, chunks, count, wave_in_group(), waves));
-  if (threadIdx.x == 0) close_norm(control, a, s);
+  if (threadIdx.x == 0) close_norm(control, a, opening, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -367,9 +385,10 @@ __device__ __forceinline__ void adamw_f32_piece(const OptimTensor& t, const Adam
 template <int ET>
 __global__ __launch_bounds__(kWave) void adamw_f32_kernel(const OptimTensor* tensors, const OptimChunk* chunks,
                                                           const gb_optim_control* control, AdamArgs a) {
-  if (control->skip != 0) return;
   const Piece w = step_piece(tensors, chunks);
-  if (w.first >= w.t.n) return;
+  // one test, so that the control block's line and the tables' are on their
+  // way together
+  if ((control->skip != 0) | (w.first >= w.t.n)) return;
   const Rates r = tensor_rates(control, w.t);
   const size_t i = w.first + threadIdx.x * 4;
   if (w.first + kBlock <= w.t.n) adamw_f32_piece<ET, true>(w.t, a, r, i);
@@ -489,9 +508,10 @@ __device__ __forceinline__ void adamw_e4m3_block(const OptimTensor& t, const Ada
 template <int ET>
 __global__ __launch_bounds__(kWave) void adamw_e4m3_kernel(const OptimTensor* tensors, const OptimChunk* chunks,
                                                            const gb_optim_control* control, AdamArgs a) {
-  if (control->skip != 0) return;
   const Piece w = step_piece(tensors, chunks);
-  if (w.first >= w.t.n) return;
+  // one test, so that the control block's line and the tables' are on their
+  // way together
+  if ((control->skip != 0) | (w.first >= w.t.n)) return;
   const Rates r = tensor_rates(control, w.t);
   if (w.first + kBlock <= w.t.n) adamw_e4m3_block<ET, true>(w.t, a, r, control->key, w.first);
   else adamw_e4m3_block<ET, false>(w.t, a, r, control->key, w.first);

@@ -420,3 +420,43 @@ def test_a_tensor_beyond_32_bit_offsets(gb, bits):
     same(f32(ms[-hms.size:]), hms, "m_scale")
     same(f32(vs[-hvs.size:]), hvs, "v_scale")
     assert not bool(p[:n - tail].any()) and not bool(m[:n - tail].any())
+
+
+def test_the_binding_refuses_what_does_not_fit(gb):
+    """Each with nothing enqueued: wrong types, sizes, strides and devices."""
+    n = 1000
+    f = lambda k=n, dt=torch.float32: torch.zeros(k, dtype=dt, device=DEV)  # noqa: E731
+    ws = f(gb.gb_optim_plan_bytes([n]), torch.uint8)
+    good = gb.GbOptimTensor(f(), f(), f(), f())
+    coded = gb.GbOptimTensor(f(), f(), f(n, torch.uint8), f(n, torch.uint8), f(4), f(4))
+    for bad, error, text in (
+            (good._replace(param=f(n, torch.float16)), TypeError, "param must be torch.float32"),
+            (good._replace(grad=f(n, torch.float64)), TypeError, "grad must be"),
+            (good._replace(grad=f(n - 1)), ValueError, "grad has 999 elements"),
+            (good._replace(m=f(n + 1)), ValueError, r"\.m has 1001 elements"),
+            (good._replace(v=f(2 * n)[::2]), ValueError, r"\.v must be contiguous"),
+            (good._replace(m=f(n, torch.bfloat16)), TypeError, r"\.m must be torch.float32"),
+            (good._replace(param=torch.zeros(n)), ValueError, "param must be in device memory"),
+            (good._replace(param=None), TypeError, "param must be a torch.Tensor"),
+            (good._replace(copy=f(n, torch.float16)), TypeError, "copy must be torch.float32"),
+            (good._replace(m_scale=f(4)), gb.GbError, "scales, but float32"),
+            (coded._replace(v=f()), TypeError, r"\.v must be torch.uint8"),
+            (coded._replace(v_scale=None), TypeError, "v_scale must be a torch.Tensor"),
+            (coded._replace(m_scale=f(3)), ValueError, "m_scale has 3 elements, expected 4")):
+        with pytest.raises(error, match=text):
+            gb.gb_optim_plan([bad], ws)
+    with pytest.raises(gb.GbError, match="workspace"):
+        gb.gb_optim_plan([good], ws[:256])
+    with pytest.raises(gb.GbError, match="overlaps"):
+        gb.gb_optim_plan([good._replace(grad=good.param)], ws)
+    plan = gb.gb_optim_plan([good, coded], f(gb.gb_optim_plan_bytes([n, n]), torch.uint8))
+    control = torch.zeros(64, dtype=torch.uint8, device=DEV)
+    for bad, error in ((control[:32], ValueError), (control.view(torch.float32), TypeError), (control.cpu(), ValueError),
+                       (None, TypeError)):
+        with pytest.raises(error):
+            gb.gb_adamw_step(plan, bad)
+    with pytest.raises(gb.GbError, match="inv_scale"):
+        gb.gb_optim_begin(plan, control, 0.0)
+    with pytest.raises(gb.GbError, match="max_norm"):
+        gb.gb_optim_begin_clip(plan, control, -1.0)
+    assert not bool(host(control).any())
