@@ -70,8 +70,8 @@ _SP = ctypes.POINTER(ctypes.c_size_t)
 class _OptimTensor(ctypes.Structure):
     """gb_optim_tensor of include/gbreduce.h."""
     _fields_ = [("n", _S), ("param", _P), ("grad", _P), ("copy", _P), ("m", _P), ("v", _P), ("m_scale", _P),
-                ("v_scale", _P), ("dtype", _I), ("state", _I), ("lr_scale", ctypes.c_float),
-                ("weight_decay", ctypes.c_float)]
+                ("v_scale", _P), ("dtype", _I), ("copy_dtype", _I), ("state", _I), ("reserved", _I),
+                ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float)]
 
 
 class _OptimHandle(ctypes.Structure):
@@ -566,7 +566,7 @@ GbOptimTensor = collections.namedtuple(
 GbOptimTensor.__doc__ = """One tensor of an optimizer plan: param (float32), grad (float32, float16 or
 bfloat16), and the moments: m and v float32, or uint8 E4M3 codes of m and
 sqrt(v) with float32 scales m_scale and v_scale, one per 256 values.  copy
-(float16 or bfloat16, grad's type) receives the updated parameters rounded;
+(float16 or bfloat16) receives the updated parameters rounded;
 lr_scale multiplies the control block's learning rate; weight_decay is
 decoupled.  All zeros is the moments' state before the first step."""
 
@@ -607,6 +607,9 @@ def _optim_entry(i, t, device):
     _optim_part(param, torch.float32, n := param.numel() if isinstance(param, torch.Tensor) else 0, device, i, "param")
     if not isinstance(grad, torch.Tensor) or grad.dtype not in _OPTIM_TYPES:
         raise TypeError(f"tensors[{i}].grad must be a tensor of one of {list(_OPTIM_TYPES)}")
+    copy_type = copy.dtype if isinstance(copy, torch.Tensor) else torch.bfloat16
+    if copy_type not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"tensors[{i}].copy must be torch.float16 or torch.bfloat16, not {copy_type}")
     coded = isinstance(m, torch.Tensor) and m.dtype is torch.uint8
     moment = torch.uint8 if coded else torch.float32
     blocks = (n + GB_BLOCK - 1) // GB_BLOCK
@@ -614,9 +617,10 @@ def _optim_entry(i, t, device):
     scales = [_optim_part(x, torch.float32, blocks if coded else x.numel(), device, i, part) if coded or x is not None
               else None for x, part in ((m_scale, "m_scale"), (v_scale, "v_scale"))]
     return (n, param.data_ptr(), _optim_part(grad, grad.dtype, n, device, i, "grad"),
-            None if copy is None else _optim_part(copy, grad.dtype, n, device, i, "copy"),
+            None if copy is None else _optim_part(copy, copy_type, n, device, i, "copy"),
             _optim_part(m, moment, n, device, i, "m"), _optim_part(v, moment, n, device, i, "v"), *scales,
-            _OPTIM_TYPES[grad.dtype], GB_STATE_E4M3 if coded else GB_STATE_F32, lr_scale, weight_decay)
+            _OPTIM_TYPES[grad.dtype], _OPTIM_TYPES.get(copy_type, 0), GB_STATE_E4M3 if coded else GB_STATE_F32, 0,
+            lr_scale, weight_decay)
 
 
 def gb_optim_plan(tensors, workspace, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, stream=None):

@@ -30,7 +30,7 @@ struct OptimTensor {
   float* ms;
   float* vs;
   uint32_t first_block;  // of 256 values, in the plan: where the dither counts from
-  uint32_t dtype;
+  uint32_t types;        // the gradient's dtype, and the copy's from bit 16: a whole word, which the scalar unit loads
   float lr_scale;
   float weight_decay;
 };

@@ -126,11 +126,11 @@ __device__ __forceinline__ f4 load_grad4(const void* p, size_t i, size_t n) {
     return f4{(float)h.x, (float)h.y, (float)h.z, (float)h.w};
   }
 }
-// v, whose NaNs are canonical, rounded to a 2-byte type.
-template <int ET, bool FULL>
-__device__ __forceinline__ void store_copy4(void* p, size_t i, size_t n, f4 v) {
-  static_assert(ET != GB_DTYPE_F32, "a copy is of a 2-byte type");
-  if constexpr (ET == GB_DTYPE_BF16) {
+// v, whose NaNs are canonical, rounded to the tensor's copy.
+template <bool FULL>
+__device__ __forceinline__ void store_copy4(const OptimTensor& t, size_t i, size_t n, f4 v) {
+  void* p = t.copy;
+  if (t.types >> 16 == GB_DTYPE_BF16) {
     // the converting instruction rounds to nearest even, two values at a
     // time, where bf16_pack4 takes seven instructions a value
     typedef __bf16 b4 __attribute__((ext_vector_type(4)));
@@ -264,8 +264,9 @@ __device__ __forceinline__ double wave_squares(const OptimTensor* tensors, const
     const OptimChunk c = next;
     if (b + waves < count) next = chunks[b + waves];
     const OptimTensor& t = tensors[c.tensor];
-    if (t.dtype == GB_DTYPE_F32) s = chunk_squares<GB_DTYPE_F32, KEEP>(t, c.chunk, s);
-    else if (t.dtype == GB_DTYPE_F16) s = chunk_squares<GB_DTYPE_F16, KEEP>(t, c.chunk, s);
+    const uint32_t dtype = t.types & 0xFFFFu;
+    if (dtype == GB_DTYPE_F32) s = chunk_squares<GB_DTYPE_F32, KEEP>(t, c.chunk, s);
+    else if (dtype == GB_DTYPE_F16) s = chunk_squares<GB_DTYPE_F16, KEEP>(t, c.chunk, s);
     else s = chunk_squares<GB_DTYPE_BF16, KEEP>(t, c.chunk, s);
   }
   return s;
@@ -377,9 +378,7 @@ __device__ __forceinline__ void adamw_f32_piece(const OptimTensor& t, const Adam
   store_f4<f4_any, FULL>(t.p, i, n, p);
   store_f4<f4, FULL>(static_cast<float*>(t.m), i, n, canon4(m));
   store_f4<f4, FULL>(static_cast<float*>(t.v), i, n, canon4(v));
-  if constexpr (ET != GB_DTYPE_F32) {
-    if (t.copy != nullptr) store_copy4<ET, FULL>(t.copy, i, n, p);
-  }
+  if (t.copy != nullptr) store_copy4<FULL>(t, i, n, p);
 }
 
 template <int ET>
@@ -476,9 +475,7 @@ __device__ __forceinline__ void adamw_e4m3_block(const OptimTensor& t, const Ada
     utop = wave_absmax(finite4(u));
   }
   store_f4<f4_any, FULL>(t.p, i, n, p);
-  if constexpr (ET != GB_DTYPE_F32) {
-    if (t.copy != nullptr) store_copy4<ET, FULL>(t.copy, i, n, p);
-  }
+  if (t.copy != nullptr) store_copy4<FULL>(t, i, n, p);
 
   const int me = scale_exponent(mtop), ue = scale_exponent(utop);
   const f4 mq = m * pow2(-me);

@@ -95,10 +95,10 @@ gb_status check_tensor(const gb_optim_tensor& t, const char* fn, int i) {
     return fail(GB_ERR_INVALID_ARG, "%s: tensors[%d] has scales, but float32 moments", fn, i);
   }
   if (t.copy != nullptr) {
-    if (t.dtype == GB_DTYPE_F32) {
-      return fail(GB_ERR_UNSUPPORTED, "%s: tensors[%d] has a copy, but its type is float32", fn, i);
+    if (t.copy_dtype != GB_DTYPE_F16 && t.copy_dtype != GB_DTYPE_BF16) {
+      return fail(GB_ERR_UNSUPPORTED, "%s: tensors[%d].copy_dtype %d is not float16 or bfloat16", fn, i, t.copy_dtype);
     }
-    if ((s = check_pointer(t.copy, elem_size(t.dtype), fn, i, "copy")) != GB_OK) return s;
+    if ((s = check_pointer(t.copy, elem_size(t.copy_dtype), fn, i, "copy")) != GB_OK) return s;
   }
   return GB_OK;
 }
@@ -107,7 +107,7 @@ void add_spans(const gb_optim_tensor& t, long i, gb::Spans* outs, gb::Spans* ins
   const bool coded = t.state == GB_STATE_E4M3;
   const size_t moment = coded ? t.n : 4 * t.n, scales = 4 * nblocks(t.n);
   outs->add(t.param, 4 * t.n, "param", i);
-  outs->add(t.copy, elem_size(t.dtype) * t.n, "copy", i);
+  outs->add(t.copy, elem_size(t.copy_dtype) * t.n, "copy", i);
   outs->add(t.m, moment, "m", i);
   outs->add(t.v, moment, "v", i);
   if (coded) {
@@ -190,8 +190,8 @@ gb_status make_plan(const char* fn, gb_optim_handle* handle, const gb_optim_tens
     const gb_optim_tensor& t = tensors[i];
     gb::OptimTensor d = {};
     if (t.n != 0) {
-      d = {t.n, t.param, t.grad, t.copy, t.m, t.v, t.m_scale, t.v_scale, (uint32_t)block, (uint32_t)t.dtype,
-           t.lr_scale, t.weight_decay};
+      d = {t.n, t.param, t.grad, t.copy, t.m, t.v, t.m_scale, t.v_scale, (uint32_t)block,
+           (uint32_t)t.dtype | (t.copy != nullptr ? (uint32_t)t.copy_dtype << 16 : 0u), t.lr_scale, t.weight_decay};
       uint32_t& at = next[gb::optim_kind(t.dtype, t.state)];
       up.first_chunk[up.count] = at;
       at += (uint32_t)nchunks(t.n);

@@ -647,13 +647,15 @@ typedef struct gb_optim_tensor {
   size_t n;           /* values; 0 leaves the tensor out (its pointers are not looked at) */
   float* param;       /* read and written                                     */
   const void* grad;   /* read; dtype                                          */
-  void* copy;         /* NULL, or n values of dtype, written: the model's low-precision parameters */
+  void* copy;         /* NULL, or n values of copy_dtype, written: the model's low-precision parameters */
   void* m;            /* read and written, as state says                      */
   void* v;
   float* m_scale;     /* GB_STATE_E4M3: ceil(n / 256) scales each; else NULL  */
   float* v_scale;
-  int dtype;          /* GB_DTYPE_F32, F16 or BF16; a copy needs F16 or BF16  */
+  int dtype;          /* of grad: GB_DTYPE_F32, F16 or BF16                   */
+  int copy_dtype;     /* of copy: GB_DTYPE_F16 or BF16; not looked at without one */
   int state;          /* gb_optim_state                                       */
+  int reserved;       /* 0                                                    */
   float lr_scale;     /* factor of the control block's lr (parameter groups)  */
   float weight_decay; /* decoupled: p is scaled by 1 - lr_t * weight_decay    */
 } gb_optim_tensor;

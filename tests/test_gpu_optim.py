@@ -63,7 +63,7 @@ class Problem:
             p = room(torch.float32, n, shift)
             g = room(dt, n, shift)
             p.copy_(torch.from_numpy(rng.standard_normal(n, dtype=np.float32) * np.float32(0.02)))
-            c = room(dt, n, shift) if copy else None
+            c = room(TYPES[copy] if isinstance(copy, str) else dt, n, shift) if copy else None
             blocks = -(-n // 256)
             if state == "e4m3":
                 m, v = room(torch.uint8, n, 0), room(torch.uint8, n, 0)
@@ -175,6 +175,18 @@ def test_kinds_mixed_in_one_plan_with_empty_tensors(gb):
             for state in ("f32", "e4m3"):
                 spec.append((n, kind, state, kind == "bf16"))
     prob = Problem(gb, spec, 4)
+    for _ in range(2):
+        prob.gradients()
+        prob.step(1.0)
+        prob.follow(1.0)
+        prob.check()
+
+
+@pytest.mark.parametrize("state", ["f32", "e4m3"])
+def test_copies_of_either_type_beside_every_gradient_type(gb, state):
+    """A bfloat16 model trained on float32 gradients, and the other pairs."""
+    spec = [(n, kind, state, copy) for n in (1, 255, 3001) for kind in ("f32", "f16", "bf16") for copy in ("f16", "bf16")]
+    prob = Problem(gb, spec, 60, shift=1)
     for _ in range(2):
         prob.gradients()
         prob.step(1.0)
@@ -438,7 +450,8 @@ def test_the_binding_refuses_what_does_not_fit(gb):
             (good._replace(m=f(n, torch.bfloat16)), TypeError, r"\.m must be torch.float32"),
             (good._replace(param=torch.zeros(n)), ValueError, "param must be in device memory"),
             (good._replace(param=None), TypeError, "param must be a torch.Tensor"),
-            (good._replace(copy=f(n, torch.float16)), TypeError, "copy must be torch.float32"),
+            (good._replace(copy=f(n, torch.float64)), TypeError, "copy must be torch.float16 or"),
+            (good._replace(copy=f(n - 1, torch.float16)), ValueError, "copy has 999 elements"),
             (good._replace(m_scale=f(4)), gb.GbError, "scales, but float32"),
             (coded._replace(v=f()), TypeError, r"\.v must be torch.uint8"),
             (coded._replace(v_scale=None), TypeError, "v_scale must be a torch.Tensor"),

@@ -21,9 +21,9 @@ def test_constants_and_structures_match_the_header(gb):
         assert getattr(gb, name) == int(re.search(rf"#define {name} (\d+)", text).group(1))
     for name in ("GB_STATE_F32", "GB_STATE_E4M3"):
         assert getattr(gb, name) == int(re.search(rf"\b{name} = (\d+)", text).group(1))
-    assert ctypes.sizeof(gb._OptimTensor) == 80 and ctypes.sizeof(gb._OptimHandle) == 192
+    assert ctypes.sizeof(gb._OptimTensor) == 88 and ctypes.sizeof(gb._OptimHandle) == 192
     assert [f[0] for f in gb._OptimTensor._fields_] == ["n", "param", "grad", "copy", "m", "v", "m_scale", "v_scale",
-                                                       "dtype", "state", "lr_scale", "weight_decay"]
+                                                       "dtype", "copy_dtype", "state", "reserved", "lr_scale", "weight_decay"]
 
 
 def test_plan_bytes(gb):
@@ -40,7 +40,7 @@ def test_plan_bytes(gb):
 
 # made-up device addresses: a refused call looks at none of them
 GOOD = dict(n=1000, param=0x100000, grad=0x200000, copy=None, m=0x300000, v=0x400000, m_scale=None, v_scale=None,
-            dtype=0, state=0, lr_scale=1.0, weight_decay=0.0)
+            dtype=0, copy_dtype=0, state=0, reserved=0, lr_scale=1.0, weight_decay=0.0)
 CODED = dict(GOOD, m_scale=0x500000, v_scale=0x600000, state=1)
 
 
@@ -80,7 +80,8 @@ CASES = [
     ("codes without a scale", lambda gb: plan(gb, [dict(CODED, v_scale=None)]), INV, "v_scale is NULL"),
     ("a misaligned scale", lambda gb: plan(gb, [dict(CODED, v_scale=0x600002)]), MIS, "v_scale"),
     ("a float32 copy", lambda gb: plan(gb, [dict(GOOD, copy=0x700000)]), UNS, "copy"),
-    ("a misaligned copy", lambda gb: plan(gb, [dict(GOOD, dtype=2, copy=0x700001)]), MIS, "copy"),
+    ("a misaligned copy", lambda gb: plan(gb, [dict(GOOD, copy_dtype=2, copy=0x700001)]), MIS, "copy"),
+    ("a copy of an unknown type", lambda gb: plan(gb, [dict(GOOD, copy_dtype=9, copy=0x700000)]), UNS, "copy_dtype"),
     ("moments off 16 bytes", lambda gb: plan(gb, [dict(GOOD, m=0x300004)]), MIS, "m = "),
     ("codes off 16 bytes", lambda gb: plan(gb, [dict(CODED, v=0x400001)]), MIS, "v = "),
     ("a parameter off its element", lambda gb: plan(gb, [dict(GOOD, param=0x100002)]), MIS, "param"),
@@ -89,7 +90,7 @@ CASES = [
     ("two tensors in one buffer", lambda gb: plan(gb, [GOOD, GOOD]), INV, "overlaps"),
     ("a moment in the workspace", lambda gb: plan(gb, [dict(GOOD, m=0x900100)]), INV, "overlaps"),
     ("scales over codes", lambda gb: plan(gb, [dict(CODED, m_scale=0x300100)]), INV, "overlaps"),
-    ("a copy over the gradient", lambda gb: plan(gb, [dict(GOOD, dtype=2, copy=0x200002)]), INV, "overlaps"),
+    ("a copy over the gradient", lambda gb: plan(gb, [dict(GOOD, copy_dtype=2, copy=0x200002)]), INV, "overlaps"),
 ] + [(f"a NULL {f}", lambda gb, f=f: plan(gb, [dict(GOOD, **{f: None})]), INV, f"{f} is NULL")
      for f in ("param", "grad", "m", "v")]
 
