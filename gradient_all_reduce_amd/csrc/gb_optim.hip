@@ -13,10 +13,17 @@ constexpr int kWaves = kThreads / kWave;
 // Up to this many chunks the norm is one launch of one workgroup.
 constexpr uint32_t kNormSmall = 64;
 // Up to this many bytes of gradients the norm pass reads them without the
-// non-temporal hint: the step that follows then finds them in the 256 MiB
-// last-level cache.  A clipped float32 step at 67, 134, 268, 537 MB of
-// gradients takes 85, 162, 324, 684 us with the hint left out and 91, 175,
-// 358, 710 us with it; at 4 GB the norm pass alone takes 648 and 581 us.
+// non-temporal hint: the step that follows then finds some of them in the
+// 256 MiB last-level cache.  Norm and step together, hint left out / given:
+//   steps back to back, float32: 85 / 91 us at 67 MB of gradients, 162 / 175
+//     at 134, 324 / 358 at 268, 684 / 710 at 537;
+//   the gradients written last, as an all-reduce leaves them: float32 93 / 95,
+//     173 / 181, 356 / 351, 709 / 714; bfloat16 with 8-bit moments 107 / 115
+//     at 67 MB, 200 / 212 at 134, 388 / 404 at 268;
+//   1 GiB of other values written last: 102 / 94, 198 / 179, 371 / 338, 718 /
+//     670, since reads that stay in the cache push those values out first.
+// At 4 GB of gradients, which the cache cannot hold, the norm pass alone
+// takes 648 us without the hint and 581 with it.
 constexpr size_t kNormKeepBytes = (size_t)640 << 20;
 
 // ---------------------------------------------------------------------------
@@ -346,13 +353,17 @@ __device__ __forceinline__ void adamw4(const AdamArgs& a, const Rates& r, f4 g, 
 // lanes below 2^32.
 constexpr uint32_t kPerChunk = kOptimChunk / kBlock;
 constexpr uint32_t kLaunchChunks = 1u << 23;
-// The float32 step holds LDS it does not use, so that 16 workgroups share a
-// CU: 64-lane workgroups leave room for 32, and the fewer streams at once
-// gain 1.0-2.5% (67M bfloat16 values with a copy: 304 to 297 us; 1e9 float32
-// values: 4,560 to 4,510 us; 10 or 8 per CU lose again).  The 8-bit step is
-// bound by its arithmetic as well and wants every wavefront it can have (8%
-// slower with 20 per CU).
-constexpr unsigned kSixteenPerCuLds = 10u << 10;
+// The float32 step holds LDS it does not use, so that 14 workgroups share a
+// CU, and 12 from 2^27 values in a launch; 64-lane workgroups leave room for
+// 32, and fewer streams at once read and write faster.  Uncapped against 16:
+// 67M bfloat16 values with a copy 304 against 297 us.  16, 14 and 12 per CU:
+// 2^24 float32 values 78.2, 78.8, 81.4 us; 2^26 300, 295, 290; 2^27 589, 582,
+// 576; 2^29 2,364, 2,339, 2,301; bfloat16 with a copy 79.2, 79.4, 80.8; 300,
+// 299, 301; 603, 593, 587; 2,446, 2,445, 2,419.  10 and 8 lose 3% and more.
+// The 8-bit step, with less than half the bytes in flight per wavefront,
+// wants every wavefront it can have (5% slower with 20 per CU).
+constexpr unsigned kFourteenPerCuLds = 11520, kTwelvePerCuLds = 13u << 10;
+constexpr uint32_t kTwelveFromChunks = (uint32_t)(((size_t)1 << 27) / kOptimChunk);
 using StepOrder = GroupOrder<8, 1024, 1>;
 
 struct Piece {
@@ -562,8 +573,8 @@ hipError_t launch_adamw(const OptimPlan& plan, const gb_optim_control* control, 
   for (int k = 0; k < kOptimKinds; k++) {
     for (uint32_t c = plan.first[k]; c < plan.first[k + 1]; c += kLaunchChunks) {
       const uint32_t left = plan.first[k + 1] - c, count = left < kLaunchChunks ? left : kLaunchChunks;
-      kernels[k]<<<count * kPerChunk, kWave, k < 3 ? kSixteenPerCuLds : 0, stream>>>(plan.tensors, plan.chunks + c,
-                                                                                     control, a);
+      const unsigned lds = k >= 3 ? 0 : count < kTwelveFromChunks ? kFourteenPerCuLds : kTwelvePerCuLds;
+      kernels[k]<<<count * kPerChunk, kWave, lds, stream>>>(plan.tensors, plan.chunks + c, control, a);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
