@@ -1085,7 +1085,7 @@ __host__ __device__ constexpr unsigned fused_bf16_lds(int k, size_t n) {
 size_t ceil_div(size_t a, size_t b) { return (a + b - 1) / b; }
 
 // Workgroups for one lane per `per_lane` values, or 0 if too many.
-[[maybe_unused]] size_t grid_for(size_t n, size_t per_lane) {
+size_t grid_for(size_t n, size_t per_lane) {
   const size_t g = ceil_div(ceil_div(n, per_lane), (size_t)kThreads);
   return g > kMaxGrid ? 0 : g;
 }

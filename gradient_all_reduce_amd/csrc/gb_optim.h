@@ -11,7 +11,9 @@
 
 namespace gb {
 
-// Values per chunk of a tensor: the unit of work of a workgroup.
+// Values per chunk of a tensor: what one wavefront of the norm pass takes at a
+// time, four vectors per lane, and four wavefronts of the step.  The table of
+// chunks costs 8 bytes for each, below 0.1% of the step's traffic.
 constexpr size_t kOptimChunk = 1024;
 
 // A kind is the combination of gradient type and state that one step kernel

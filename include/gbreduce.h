@@ -18,7 +18,8 @@
  * and, around them: AVG, MAX and MIN; the README's other element types,
  * reduced exactly or through the codecs; an error-feedback residual per
  * buffer; the bucket stream over buckets held in separate buffers, several
- * per launch; and the staged (pipelined) steps through pinned host memory.
+ * per launch; the staged (pipelined) steps through pinned host memory; and
+ * the optimizer's step on the reduced gradients (norm, clipping, AdamW).
  *
  * Conventions shared by every call
  * --------------------------------
