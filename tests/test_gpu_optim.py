@@ -216,8 +216,8 @@ def test_a_plan_of_nothing(gb):
         assert float(host(prob.view["coef"])) == 0.5 and int(host(prob.view["skip"])) == 0
 
 
-@pytest.mark.parametrize("sigma,wd", [(1e-3, 0.0), (1e3, 0.1), (1e-12, 0.1)])
-def test_float32_step_against_binary64(gb, sigma, wd):
+@pytest.mark.parametrize("sigma", [1e-3, 1e3, 1e-12])
+def test_float32_step_against_binary64(gb, sigma):
     prob = Problem(gb, [(20011, "f32", "f32", False)], 23, sigma=sigma)
     prob.gradients()
     prob.step()
@@ -233,6 +233,40 @@ def test_float32_step_against_binary64(gb, sigma, wd):
                              bounds(old[0], g, old[2], old[3], 2, 0.25, lr, 1.0, w)):
         assert (np.abs(f32(x).astype(np.float64) - y) <= b).all(), name
     assert h["n"] == 20011
+
+
+def code_step(q):
+    """Distance of the E4M3 codes around magnitudes q (the larger one at a border)."""
+    return np.exp2(np.maximum(np.floor(np.log2(np.maximum(q, 2.0 ** -20))), -6) - 3)
+
+
+@pytest.mark.parametrize("sigma", [1e-3, 1e3, 1e-12])
+def test_8_bit_step_against_binary64(gb, sigma):
+    """p' within the float32 step's bounds of binary64 from the decoded
+    moments; m' and the root at most one code's distance from binary64's."""
+    n = 20011
+    prob = Problem(gb, [(n, "f32", "e4m3", False)], 24, sigma=sigma)
+    for _ in range(3):
+        prob.gradients()
+        prob.step()
+        prob.follow()
+    h, e = prob.host[0], prob.entries[0]
+    p, m, u = f32(e.param), P.decode(h["m"], h["ms"]), P.decode(h["v"], h["vs"])
+    # u * u is rounded once before it is v: one more rounding of v
+    v = u.astype(np.float64) ** 2
+    prob.gradients()
+    g = f32(e.grad)
+    prob.step(inv_scale=0.5)
+    lr, w = float(np.float32(1e-3)), float(np.float32(0.1))
+    want = P.adamw64(p, g, m, v, 4, 0.5, lr, 1.0, w)
+    bp, bm, bv = bounds(p, g, m, v, 4, 0.5, lr, 1.0, w)
+    assert (np.abs(f32(e.param) - want[0]) <= bp).all()
+    mags = np.append(P.E4M3, np.nan)
+    for codes, scale, exact, err in ((e.m, e.m_scale, want[1], bm), (e.v, e.v_scale, np.sqrt(want[2]), np.sqrt(bv))):
+        c, sc = host(codes).numpy(), np.repeat(f32(scale).astype(np.float64), 256)[:n]
+        got = np.where(c & 0x80, -mags[c & 0x7F], mags[c & 0x7F]) * sc
+        near = code_step(np.maximum(np.abs(got), np.abs(exact)) / sc) * sc
+        assert (np.abs(got - exact) <= near + err).all()
 
 
 @pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
