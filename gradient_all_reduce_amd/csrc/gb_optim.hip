@@ -201,13 +201,20 @@ struct Opening {
   float rate1, rate2;
   uint32_t key;
 };
+// 1 / (1 - b^t), or 1 / sqrt(1 - b^t).
+__device__ float bias_rate(double b, int64_t t, bool root) {
+  const double x = 1.0 - power(b, t);
+  return (float)(1.0 / (root ? sqrt(x) : x));
+}
+__device__ uint32_t dither_key(uint64_t seed, int64_t t) {
+  constexpr uint64_t kGolden = 0x9E3779B97F4A7C15ull;
+  uint64_t z = seed + (uint64_t)t * kGolden;
+  for (int i = 0; i < 3; i++) z = (z ^ (z >> 32)) * kGolden;
+  return (uint32_t)(z >> 32);
+}
 __device__ Opening next_step(const gb_optim_control* c, const StepArgs& a) {
   const int64_t t = c->step + 1;
-  constexpr uint64_t kGolden = 0x9E3779B97F4A7C15ull;
-  uint64_t z = a.seed + (uint64_t)t * kGolden;
-  for (int i = 0; i < 3; i++) z = (z ^ (z >> 32)) * kGolden;
-  return Opening{t, (float)(1.0 / (1.0 - power(a.beta1, t))), (float)(1.0 / sqrt(1.0 - power(a.beta2, t))),
-                 (uint32_t)(z >> 32)};
+  return Opening{t, bias_rate(a.beta1, t, false), bias_rate(a.beta2, t, true), dither_key(a.seed, t)};
 }
 __device__ void open_step(gb_optim_control* c, const Opening& o, float coef) {
   c->step = o.step;
@@ -218,8 +225,19 @@ __device__ void open_step(gb_optim_control* c, const Opening& o, float coef) {
   c->key = o.key;
 }
 
-__global__ void optim_begin_kernel(gb_optim_control* c, StepArgs a) {
-  open_step(c, next_step(c, a), (float)a.inv_scale);
+// Two lanes, one for each rate.
+__global__ __launch_bounds__(kWave) void optim_begin_kernel(gb_optim_control* c, StepArgs a) {
+  const int64_t t = c->step + 1;
+  const bool second = threadIdx.x != 0;
+  const float rate = bias_rate(second ? a.beta2 : a.beta1, t, second);
+  if (second) c->rate2 = rate;
+  else {
+    c->rate1 = rate;
+    c->step = t;
+    c->skip = 0;
+    c->coef = (float)a.inv_scale;
+    c->key = dither_key(a.seed, t);
+  }
 }
 
 __device__ void close_norm(gb_optim_control* c, const StepArgs& a, const Opening& o, double sum) {
@@ -569,7 +587,7 @@ hipError_t launch_optim_upload(OptimTensor* tensors, OptimChunk* chunks, const O
 hipError_t launch_optim_begin(const OptimPlan& plan, gb_optim_control* control, double inv_scale,
                               hipStream_t stream) {
   (void)hipGetLastError();
-  optim_begin_kernel<<<1, 1, 0, stream>>>(control, step_args(plan, 0.0, inv_scale));
+  optim_begin_kernel<<<1, 2, 0, stream>>>(control, step_args(plan, 0.0, inv_scale));
   return hipGetLastError();
 }
 
