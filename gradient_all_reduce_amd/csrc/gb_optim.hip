@@ -60,29 +60,45 @@ __device__ __forceinline__ GB_GLOBAL V* global_at(T* p, size_t i) {
   return (GB_GLOBAL V*)(p + i);
 }
 
+// A lane's four values.  ANY: aligned to the element only.  The under-aligned
+// types are named where the access is made: given as a template argument a
+// type loses its alignment attribute, and the access would promise 16 bytes.
 // KEEP: without the non-temporal hint, so that a later pass over the same
 // values finds them in the last-level cache.
-template <class V, bool KEEP>
-__device__ __forceinline__ V load_vec(const GB_GLOBAL V* p) {
-  if constexpr (KEEP) return *p;
-  else return __builtin_nontemporal_load(p);
+template <bool ANY, bool KEEP>
+__device__ __forceinline__ f4 load_vec4(const float* p, size_t i) {
+  if constexpr (ANY) {
+    const GB_GLOBAL f4_any* v = (const GB_GLOBAL f4_any*)(p + i);
+    if constexpr (KEEP) return *v;
+    else return __builtin_nontemporal_load(v);
+  } else {
+    const GB_GLOBAL f4* v = (const GB_GLOBAL f4*)(p + i);
+    if constexpr (KEEP) return *v;
+    else return __builtin_nontemporal_load(v);
+  }
+}
+template <bool KEEP>
+__device__ __forceinline__ u2 load_vec4(const uint16_t* p, size_t i) {
+  const GB_GLOBAL u2_any* v = (const GB_GLOBAL u2_any*)(p + i);
+  if constexpr (KEEP) return *v;
+  else return __builtin_nontemporal_load(v);
 }
 
-// Values [i, i + 4), zero at and beyond n; V is f4, or f4_any where only the
-// element is aligned.
-template <class V, bool FULL, bool KEEP = false>
+// Values [i, i + 4), zero at and beyond n.
+template <bool ANY, bool FULL, bool KEEP = false>
 __device__ __forceinline__ f4 load_f4(const float* p, size_t i, size_t n) {
-  if (FULL || i + 4 <= n) return load_vec<V, KEEP>(global_at<V>(p, i));
+  if (FULL || i + 4 <= n) return load_vec4<ANY, KEEP>(p, i);
   f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int e = 0; e < 3; e++) {
     if (i + e < n) v[e] = *global_at<float>(p, i + e);
   }
   return v;
 }
-template <class V, bool FULL>
+template <bool ANY, bool FULL>
 __device__ __forceinline__ void store_f4(float* p, size_t i, size_t n, f4 v) {
   if (FULL || i + 4 <= n) {
-    __builtin_nontemporal_store((V)v, global_at<V>(p, i));
+    if constexpr (ANY) __builtin_nontemporal_store(v, (GB_GLOBAL f4_any*)(p + i));
+    else __builtin_nontemporal_store(v, (GB_GLOBAL f4*)(p + i));
     return;
   }
   for (int e = 0; e < 3; e++) {
@@ -93,7 +109,7 @@ __device__ __forceinline__ void store_f4(float* p, size_t i, size_t n, f4 v) {
 template <bool FULL, bool KEEP = false>
 __device__ __forceinline__ u2 load_half4(const void* p, size_t i, size_t n) {
   const uint16_t* h = static_cast<const uint16_t*>(p);
-  if (FULL || i + 4 <= n) return load_vec<u2_any, KEEP>(global_at<u2_any>(h, i));
+  if (FULL || i + 4 <= n) return load_vec4<KEEP>(h, i);
   uint32_t w[2] = {0u, 0u};
   for (int e = 0; e < 3; e++) {
     if (i + e < n) w[e >> 1] |= (uint32_t)*global_at<uint16_t>(h, i + e) << (16 * (e & 1));
@@ -104,7 +120,7 @@ template <bool FULL>
 __device__ __forceinline__ void store_half4(void* p, size_t i, size_t n, u2 w) {
   uint16_t* h = static_cast<uint16_t*>(p);
   if (FULL || i + 4 <= n) {
-    __builtin_nontemporal_store((u2_any)w, global_at<u2_any>(h, i));
+    __builtin_nontemporal_store(w, (GB_GLOBAL u2_any*)(h + i));
     return;
   }
   const uint32_t ws[2] = {w.x, w.y};
@@ -138,7 +154,7 @@ __device__ __forceinline__ void store_codes(void* p, size_t i, size_t n, uint32_
 template <int ET, bool FULL, bool KEEP = false>
 __device__ __forceinline__ f4 load_grad4(const void* p, size_t i, size_t n) {
   if constexpr (ET == GB_DTYPE_F32) {
-    return load_f4<f4_any, FULL, KEEP>(static_cast<const float*>(p), i, n);
+    return load_f4<true, FULL, KEEP>(static_cast<const float*>(p), i, n);
   } else {
     const u2 w = load_half4<FULL, KEEP>(p, i, n);
     if constexpr (ET == GB_DTYPE_BF16) return bf16_unpack4(w);
@@ -418,15 +434,15 @@ template <int ET, bool FULL>
 __device__ __forceinline__ void adamw_f32_piece(const OptimTensor& t, const AdamArgs& a, const Rates& r, size_t i) {
   const size_t n = t.n;
   const f4 g = load_grad4<ET, FULL>(t.g, i, n);
-  f4 p = load_f4<f4_any, FULL>(t.p, i, n);
-  f4 m = load_f4<f4, FULL>(static_cast<const float*>(t.m), i, n);
-  f4 v = load_f4<f4, FULL>(static_cast<const float*>(t.v), i, n);
+  f4 p = load_f4<true, FULL>(t.p, i, n);
+  f4 m = load_f4<false, FULL>(static_cast<const float*>(t.m), i, n);
+  f4 v = load_f4<false, FULL>(static_cast<const float*>(t.v), i, n);
   f4 u;
   adamw4(a, r, g, p, m, v, u);
   p = canon4(p);
-  store_f4<f4_any, FULL>(t.p, i, n, p);
-  store_f4<f4, FULL>(static_cast<float*>(t.m), i, n, canon4(m));
-  store_f4<f4, FULL>(static_cast<float*>(t.v), i, n, canon4(v));
+  store_f4<true, FULL>(t.p, i, n, p);
+  store_f4<false, FULL>(static_cast<float*>(t.m), i, n, canon4(m));
+  store_f4<false, FULL>(static_cast<float*>(t.v), i, n, canon4(v));
   if (t.copy != nullptr) store_copy4<FULL>(t, i, n, p);
 }
 
@@ -510,7 +526,7 @@ __device__ __forceinline__ void adamw_e4m3_block(const OptimTensor& t, const Ada
                                                  uint32_t key, size_t first) {
   const size_t n = t.n, block = first / kBlock, i = first + threadIdx.x * 4;
   const f4 g = load_grad4<ET, FULL>(t.g, i, n);
-  f4 p = load_f4<f4_any, FULL>(t.p, i, n);
+  f4 p = load_f4<true, FULL>(t.p, i, n);
   const uint32_t mw = load_codes<FULL>(t.m, i, n), vw = load_codes<FULL>(t.v, i, n);
   // The scales come as vector loads although their address is the same in
   // every lane: 4 bytes a block through the scalar cache made the step 6%
@@ -532,7 +548,7 @@ __device__ __forceinline__ void adamw_e4m3_block(const OptimTensor& t, const Ada
     mtop = wave_absmax(finite4(m));
     utop = wave_absmax(finite4(u));
   }
-  store_f4<f4_any, FULL>(t.p, i, n, p);
+  store_f4<true, FULL>(t.p, i, n, p);
   if (t.copy != nullptr) store_copy4<FULL>(t, i, n, p);
 
   const int me = scale_exponent(mtop), ue = scale_exponent(utop);
