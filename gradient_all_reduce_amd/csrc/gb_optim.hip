@@ -241,11 +241,13 @@ __device__ void open_step(gb_optim_control* c, const Opening& o, float coef) {
   c->key = o.key;
 }
 
-// Two lanes, one for each rate.
+// Two lanes, one for each rate.  Both read the step count that one of them
+// then writes, hence the barrier (in one wavefront, a wait).
 __global__ __launch_bounds__(kWave) void optim_begin_kernel(gb_optim_control* c, StepArgs a) {
   const int64_t t = c->step + 1;
   const bool second = threadIdx.x != 0;
   const float rate = bias_rate(second ? a.beta2 : a.beta1, t, second);
+  __syncthreads();
   if (second) c->rate2 = rate;
   else {
     c->rate1 = rate;

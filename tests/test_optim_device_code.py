@@ -1,7 +1,8 @@
 """What the optimizer's kernels promise the compiler, read from the device IR
 that the library's own flags give for gfx950 (CPU only, needs hipcc):
 accesses to parameters, gradients and copies assume the alignment of one
-element and no more, since these may be views into a bucket."""
+element and no more, since these may be views into a bucket; and the lanes
+that open a step read the control block before any of them writes it."""
 import os
 import re
 import subprocess
@@ -82,3 +83,14 @@ def test_views_off_16_bytes_are_accessed_at_their_elements_alignment(kernels, na
             assert align == {16: 4, 8: 2}[size], (field, size, align)
         else:
             assert name in F32_KERNELS and field in ("m", "v") and (size, align) == (16, 16)
+
+
+def test_every_lane_reads_the_step_count_before_one_writes_it(kernels):
+    """optim_begin_kernel's lanes all read control->step and one of them adds
+    to it: a barrier stands between."""
+    body = kernel(kernels, "optim_begin_kernelE")
+    loads = [i for i, line in enumerate(body) if re.search(r"= load \w+, ptr addrspace\(1\)", line)]
+    stores = [i for i, line in enumerate(body) if re.search(r"^\s+store \w+ [^,]+, ptr addrspace\(1\)", line)]
+    barriers = [i for i, line in enumerate(body) if "@llvm.amdgcn.s.barrier()" in line]
+    assert loads and stores and barriers
+    assert max(loads) < min(barriers) and max(barriers) < min(stores)
