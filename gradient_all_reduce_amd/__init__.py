@@ -638,11 +638,13 @@ def gb_optim_plan(tensors, workspace, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, 
     return GbOptimPlan(handle, tensors, workspace)
 
 
-def _control(control):
-    """Address of a control block."""
+def _control(control, plan=None):
+    """Address of a control block, which must lie on the plan's device."""
     try:
         if (control.dtype is torch.uint8 and control.is_cuda and control.numel() == GB_OPTIM_CONTROL_BYTES
                 and control.is_contiguous()):
+            if plan is not None and control.get_device() != plan.device_index:
+                raise ValueError(f"control is on {control.device}, the plan on {plan.workspace.device}")
             return control.data_ptr()
     except AttributeError:
         pass
@@ -672,19 +674,19 @@ def gb_optim_control(control):
 
 def gb_optim_begin(plan, control, inv_scale=1.0, stream=None):
     """Open a step: the gradients are scaled by inv_scale (1 / loss scale)."""
-    _check(_lib.gb_optim_begin(plan.ref, _control(control), inv_scale, _plan_stream(plan, stream)))
+    _check(_lib.gb_optim_begin(plan.ref, _control(control, plan), inv_scale, _plan_stream(plan, stream)))
 
 
 def gb_optim_begin_clip(plan, control, max_norm, inv_scale=1.0, stream=None):
     """Open a step with the global gradient norm, clipped to max_norm; a norm
     that is not finite skips the step."""
-    _check(_lib.gb_optim_begin_clip(plan.ref, _control(control), max_norm, inv_scale,
+    _check(_lib.gb_optim_begin_clip(plan.ref, _control(control, plan), max_norm, inv_scale,
                                     _plan_stream(plan, stream)))
 
 
 def gb_adamw_step(plan, control, stream=None):
     """The AdamW update of every tensor of the plan, for the step last opened."""
-    _check(_lib.gb_adamw_step(plan.ref, _control(control), _plan_stream(plan, stream)))
+    _check(_lib.gb_adamw_step(plan.ref, _control(control, plan), _plan_stream(plan, stream)))
 
 
 def gb_payload_bytes(codec, n):

@@ -129,3 +129,35 @@ def test_the_binding_refuses_host_tensors_and_wrong_types(gb):
     with pytest.raises(ValueError, match="control"):
         gb.gb_optim_control(torch.zeros(64, dtype=torch.uint8))
 
+
+
+class OnAnotherDevice:
+    """What a control block in another GPU's memory looks like to the binding."""
+    dtype, is_cuda = None, True
+
+    def __init__(self, torch):
+        self.dtype, self.device = torch.uint8, torch.device("cuda", 1)
+
+    numel = staticmethod(lambda: 64)
+    is_contiguous = staticmethod(lambda: True)
+    get_device = staticmethod(lambda: 1)
+    data_ptr = staticmethod(lambda: 0x1000)
+
+
+def made_plan(gb):
+    """A plan of no tensors on GPU 0, as gb_optim_plan leaves one."""
+    import torch
+    handle = gb._OptimHandle()
+    handle.opaque[0] = 0x67626F7074696D31
+
+    class Workspace:
+        device = torch.device("cuda", 0)
+    return gb.GbOptimPlan(handle, [], Workspace)
+
+
+def test_the_step_calls_refuse_a_control_block_of_another_device(gb):
+    import torch
+    control, plan = OnAnotherDevice(torch), made_plan(gb)
+    for call in (gb.gb_optim_begin, lambda p, c: gb.gb_optim_begin_clip(p, c, 1.0), gb.gb_adamw_step):
+        with pytest.raises(ValueError, match="control is on cuda:1, the plan on cuda:0"):
+            call(plan, control)
