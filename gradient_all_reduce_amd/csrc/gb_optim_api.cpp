@@ -213,6 +213,15 @@ gb_status check_step(const char* fn, const gb_optim_handle* handle, const void* 
   if (!aligned(control, GB_ALIGN)) {
     return fail(GB_ERR_MISALIGNED, "%s: control = %p is not %d-byte aligned", fn, control, GB_ALIGN);
   }
+  // the kernels follow the addresses in the workspace's tables (a handle of zeros but the mark has none)
+  gb::Span c, w;
+  c.lo = reinterpret_cast<uintptr_t>(control);
+  c.hi = c.lo + GB_OPTIM_CONTROL_BYTES;
+  c.name = "control";
+  w.lo = reinterpret_cast<uintptr_t>(plan->tensors);
+  w.hi = reinterpret_cast<uintptr_t>(plan->partials + gb::kNormGroups);
+  w.name = "workspace";
+  if (w.lo != 0 && c.lo < w.hi && w.lo < c.hi) return gb::overlap_error(fn, c, w);
   return GB_OK;
 }
 

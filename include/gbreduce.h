@@ -664,6 +664,8 @@ typedef struct gb_optim_tensor {
 /* The control block: GB_OPTIM_CONTROL_BYTES of device memory, 16-byte
  * aligned, zeroed by the caller before the first step, lr set by the caller
  * (and written again by stream-ordered work whenever a schedule changes it).
+ * It shares no byte with the plan's buffers: the calls refuse one inside the
+ * workspace, and the tensors' buffers are the caller's to keep apart from it.
  * Resuming: set step to the number of steps taken. */
 #define GB_OPTIM_CONTROL_BYTES 64
 typedef struct gb_optim_control {

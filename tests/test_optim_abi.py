@@ -161,3 +161,21 @@ def test_the_step_calls_refuse_a_control_block_of_another_device(gb):
     for call in (gb.gb_optim_begin, lambda p, c: gb.gb_optim_begin_clip(p, c, 1.0), gb.gb_adamw_step):
         with pytest.raises(ValueError, match="control is on cuda:1, the plan on cuda:0"):
             call(plan, control)
+
+
+def test_the_step_calls_refuse_a_control_block_inside_the_workspace(gb):
+    """The tables there hold the addresses that the kernels follow."""
+    L = gb._lib
+    made = gb._OptimHandle()
+    table, chunks, partials = 0x900000, 0x900100, 0x900200
+    end = partials + 1024 * 8
+    for word, value in enumerate((0x67626F7074696D31, table, chunks, partials)):
+        made.opaque[word] = value
+    h = ctypes.byref(made)
+    for control in (table, chunks + 16, table - 16, partials, end - 16):
+        for call in (lambda c: L.gb_optim_begin(h, c, 1.0, None), lambda c: L.gb_adamw_step(h, c, None),
+                     lambda c: L.gb_optim_begin_clip(h, c, 1.0, 1.0, None)):
+            assert call(control) == INV, hex(control)
+            assert "control overlaps workspace" in gb.gb_last_error()
+    for control in (table - 64, end):  # beside it: refused only for want of a scale
+        assert L.gb_optim_begin(h, control, 0.0, None) == INV and "inv_scale" in gb.gb_last_error()
