@@ -94,3 +94,15 @@ def test_every_lane_reads_the_step_count_before_one_writes_it(kernels):
     barriers = [i for i, line in enumerate(body) if "@llvm.amdgcn.s.barrier()" in line]
     assert loads and stores and barriers
     assert max(loads) < min(barriers) and max(barriers) < min(stores)
+
+
+def test_lds_reservations_leave_the_workgroups_they_are_named_for():
+    """LDS is handed out in granules of 1,280 bytes, 128 to a CU (counted on
+    the hardware: 11,520 bytes leave 14 workgroups, 11,521 leave 12)."""
+    text = open(os.path.join(B.CSRC, "gb_optim.hip")).read()
+    names = {"Eight": 8, "Nine": 9, "Ten": 10, "Eleven": 11, "Twelve": 12, "Fourteen": 14, "Sixteen": 16}
+    found = re.findall(r"\bk([A-Z][a-z]+)PerCuLds = ([^,;]+)[,;]", text)
+    assert found
+    for name, value in found:
+        size = eval(re.sub(r"(\d)u\b", r"\1", value), {"kLdsGranule": 1280})
+        assert 128 // -(-size // 1280) == names[name], (name, value)
