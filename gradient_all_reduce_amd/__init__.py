@@ -652,12 +652,18 @@ def _control(control, plan=None):
     raise ValueError(f"control has {control.numel()} bytes, expected {GB_OPTIM_CONTROL_BYTES}")
 
 
+# the current stream's handle without a Stream object, which takes as long to
+# make as half a launch; not every torch need have it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _plan_stream(plan, stream):
-    """Handle of the stream, or of the plan's device's current one: read
-    without making a Stream object, which takes as long as half a launch."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(plan.device_index)
+    """Handle of the stream, or of the plan's device's current one."""
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(plan.device_index)
+        stream = torch.cuda.current_stream(plan.device_index)
+    return stream.cuda_stream
 
 
 def gb_optim_control(control):

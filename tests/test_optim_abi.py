@@ -3,6 +3,8 @@ each before anything is enqueued."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 
@@ -179,3 +181,22 @@ def test_the_step_calls_refuse_a_control_block_inside_the_workspace(gb):
             assert "control overlaps workspace" in gb.gb_last_error()
     for control in (table - 64, end):  # beside it: refused only for want of a scale
         assert L.gb_optim_begin(h, control, 0.0, None) == INV and "inv_scale" in gb.gb_last_error()
+
+
+def test_the_current_stream_is_found_without_torchs_private_lookup():
+    """A torch without torch._C._cuda_getCurrentRawStream: the public one serves."""
+    code = """if True:
+        import types, torch
+        del torch._C._cuda_getCurrentRawStream
+        import gradient_all_reduce_amd as gb
+        asked = []
+        def current_stream(device):
+            asked.append(device)
+            return types.SimpleNamespace(cuda_stream=0x1234)
+        torch.cuda.current_stream = current_stream
+        plan = types.SimpleNamespace(device_index=3)
+        assert gb._plan_stream(plan, None) == 0x1234 and asked == [3]
+        assert gb._plan_stream(plan, types.SimpleNamespace(cuda_stream=5)) == 5 and asked == [3]
+        """
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
