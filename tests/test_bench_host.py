@@ -3,6 +3,7 @@ workload into one GPU's share, and when it takes HBM traffic from the
 committed rocprofv3 summaries."""
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -99,3 +100,13 @@ def test_memory_ceiling_never_takes_the_zero_data_contrast(monkeypatch, tmp_path
     got = bench.memory_ceiling()
     assert got["best_copy"] == "copy_u1_fronts_4GiB" and got["best_copy_gbs"] == 6600.0
     assert got["median_gbs"]["zeros_copy_u1_4GiB"] == 6900.0
+
+
+def test_no_workload_runs_a_kernel_source_left_out_of_the_hash():
+    """kernel_sources_sha256 leaves gb_optim.hip out since no workload runs
+    the optimizer's step: a workload that did would have to bring it in."""
+    text = open(os.path.join(ROOT, "bench.py")).read() + open(os.path.join(ROOT, "workloads.py")).read()
+    header = open(os.path.join(ROOT, "include", "gbreduce.h")).read()
+    calls = set(re.findall(r"\bgb_(?:optim|adamw)_\w+(?=\()", header))
+    assert {"gb_optim_begin", "gb_optim_begin_clip", "gb_adamw_step"} <= calls
+    assert not [c for c in calls if c in text]
