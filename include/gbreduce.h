@@ -720,7 +720,8 @@ gb_status gb_optim_begin(const gb_optim_handle* plan, void* control, double inv_
  * Squares and sums are binary64 (a binary32 gradient's square neither
  * overflows nor underflows there), added in an order fixed by the plan, so a
  * result is bit-reproducible.  If norm is not finite (a gradient is Inf or
- * NaN) the step is skipped: skip = 1, skipped + 1, coef 0, and step stays.
+ * NaN, or norm64 exceeds binary32's range) the step is skipped: skip = 1,
+ * skipped + 1, coef 0, and step stays.
  * max_norm above 0; INFINITY computes the norm and never clips.  One or two launches. */
 gb_status gb_optim_begin_clip(const gb_optim_handle* plan, void* control, double max_norm, double inv_scale,
                               void* stream);

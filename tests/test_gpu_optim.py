@@ -507,3 +507,17 @@ def test_the_binding_refuses_what_does_not_fit(gb):
     with pytest.raises(gb.GbError, match="max_norm"):
         gb.gb_optim_begin_clip(plan, control, -1.0)
     assert not bool(host(control).any())
+
+
+def test_a_norm_beyond_binary32_skips_the_step_too(gb):
+    """Finite gradients whose norm is not: four of 3e38."""
+    prob = Problem(gb, [(4, "f32", "f32", False)], 3)
+    prob.entries[0].grad.fill_(3e38)
+    prob.step(1.0)
+    prob.follow(1.0)
+    assert int(host(prob.view["skip"])) == 1 and int(host(prob.view["step"])) == 0
+    prob.check()
+    prob.step(1.0, 0.25)  # scaled by the loss scale's reciprocal it fits
+    prob.follow(1.0, 0.25)
+    assert int(host(prob.view["skip"])) == 0 and int(host(prob.view["step"])) == 1
+    prob.check()
