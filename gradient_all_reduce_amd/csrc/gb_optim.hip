@@ -6,10 +6,13 @@
 // gradient once, the step reads and writes each value of every buffer once.
 // Measured on MI355X, algorithmic bytes over kernel time, where the best plain
 // copy moves 6.6 TB/s and a plain read 7.1-7.5: the norm of 1e9 float32 values
-// 572 us (7.0 TB/s); the float32 step over them 4,342 us (6.45 TB/s); over 67M
-// values with bfloat16 gradients and copies 288 us (6.5 TB/s); the 8-bit step
-// over 1e9 such values 2,594 us (6.2 TB/s).  Counted traffic is the
-// algorithmic bytes to 0.2%.
+// 567 us (7.06 TB/s), of 1e9 bfloat16 values 299 us (6.7 TB/s); the float32 step
+// over 1e9 values 4,322 us (6.48 TB/s); over 67M values with bfloat16 gradients
+// and copies 290 us (6.5 TB/s); the 8-bit step over 1e9 such values 2,586 us
+// (6.2 TB/s).  Counted traffic over algorithmic bytes: the steps 1.0005 to 1.0013
+// from 67M values on, 1.0012 (float32) and 1.0033 (8-bit) over ragged lists of
+// 24-26M; the norm 1.008 (float32) and 1.016 (bfloat16), 32 bytes more a chunk,
+// whose 8-byte table entries share lines that several XCDs read.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Wunused-function"  // of the shared helpers, some have no use here
 #include "gb_device.h"
@@ -338,8 +341,11 @@ __device__ __forceinline__ uint32_t wave_in_group() {
 // 50 MB of gradients, and 19 us of that remain with relaxed atomics.)  Bound
 // by the reads: 1,024 workgroups, 512, 2,048 or 16,384, contiguous shares or
 // strided ones, one or two chunks at a time all stay within 3%, 6.7-7.0 TB/s
-// for 4 GB of float32.  50 MB take 14.5 us: 7 at that rate, the rest is two
-// launches' ramps.
+// for 4 GB of float32 (measured there only).  50 MB in 300 ragged bfloat16
+// tensors take 14.8 us with the second launch: 11.0 in this kernel (4.6 TB/s,
+// where the reads at full rate are 7.1 us) and 3.8 in the one that adds.
+// Most of what is lost there is lost in this kernel: 4,096 wavefronts take six
+// or seven chunks each, one after the other, table entries ahead of the data.
 template <bool KEEP>
 __global__ __launch_bounds__(kThreads) void optim_norm_kernel(const OptimTensor* tensors, const OptimChunk* chunks,
                                                               uint32_t count, double* partials) {
