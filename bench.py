@@ -1077,15 +1077,16 @@ def kernel_sources_sha256():
     """sha256 over the library's kernel sources (gb_device.h and every .hip
     file of the library that defines a kernel, by name in sorted order: each
     name, a NUL, its bytes, a NUL).  Host-only sources (the C ABI layer, the
-    no-allocation entry point), the ceiling program and the optimizer step,
-    whose kernels no workload here runs, are left out: a change there leaves
-    the workloads' kernels and their counters as they were."""
+    no-allocation entry point), the ceiling program, the optimizer step and
+    the token-sum layers, whose kernels no workload here runs, are left out: a
+    change there leaves the workloads' kernels and their counters as they were."""
     import glob
     import hashlib
     csrc = os.path.join(ROOT, "gradient_all_reduce_amd", "csrc")
     h = hashlib.sha256()
     srcs = [p for p in glob.glob(os.path.join(csrc, "*.hip"))
-            if os.path.basename(p) not in ("gb_ceiling.hip", "gb_optim.hip") and "__global__" in open(p).read()]
+            if os.path.basename(p) not in ("gb_ceiling.hip", "gb_optim.hip", "gb_norm.hip", "gb_embed.hip")
+            and "__global__" in open(p).read()]
     for path in sorted(srcs + [os.path.join(csrc, "gb_device.h")]):
         h.update(os.path.basename(path).encode() + b"\0" + open(path, "rb").read() + b"\0")
     return h.hexdigest()

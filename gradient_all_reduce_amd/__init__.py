@@ -32,7 +32,9 @@ __all__ = [
     "GB_MAX_BATCH", "gb_bucket_allreduce_local_noalloc", "GB_NOALLOC_SCRATCH_BYTES",
     "GB_STATE_F32", "GB_STATE_E4M3", "GB_OPTIM_CONTROL_BYTES", "GB_OPTIM_MAX_TENSORS", "GbOptimTensor", "GbOptimPlan",
     "gb_optim_plan_bytes", "gb_optim_plan", "gb_optim_control", "gb_optim_begin", "gb_optim_begin_clip",
-    "gb_adamw_step",
+    "gb_adamw_step", "GB_NORM_MAX_COLS", "GB_EMBEDDING_MAX_TOKENS", "GB_EMBEDDING_MAX_VOCAB", "GB_EMBEDDING_MAX_DIM",
+    "gb_layer_norm_forward", "gb_layer_norm_backward", "gb_layer_norm_workspace_bytes", "gb_embedding_forward",
+    "gb_embedding_backward", "gb_embedding_workspace_bytes",
 ]
 
 GB_OK, GB_ERR_INVALID_ARG, GB_ERR_MISALIGNED = 0, 1, 2
@@ -48,6 +50,8 @@ GB_NOALLOC_SCRATCH_BYTES = 64 << 20  # static payload scratch of gb_bucket_allre
 GB_STATE_F32, GB_STATE_E4M3 = 0, 1
 GB_OPTIM_CONTROL_BYTES = 64  # the control block of the optimizer step
 GB_OPTIM_MAX_TENSORS = 65536  # largest number of tensors of a plan
+GB_NORM_MAX_COLS = 32768  # longest row of the layer norm calls
+GB_EMBEDDING_MAX_TOKENS, GB_EMBEDDING_MAX_VOCAB, GB_EMBEDDING_MAX_DIM = 1 << 30, 2147483647, 1 << 20
 # gb_dtype of each torch element type gb_reduce_typed takes
 GB_DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float64: 3,
             torch.int8: 4, torch.uint8: 5, torch.int32: 6, torch.int64: 7}
@@ -79,7 +83,7 @@ class _OptimHandle(ctypes.Structure):
     _fields_ = [("opaque", ctypes.c_uint64 * 24)]
 
 
-_D = ctypes.c_double
+_D, _L = ctypes.c_double, ctypes.c_int64
 _SIGNATURES = {
     "gb_reduce_sum": (_I, [_P, _PP, _I, _S, _P]),
     "gb_reduce": (_I, [_P, _PP, _I, _S, _I, _I, _P]),
@@ -108,6 +112,12 @@ _SIGNATURES = {
     "gb_optim_begin": (_I, [_P, _P, _D, _P]),
     "gb_optim_begin_clip": (_I, [_P, _P, _D, _D, _P]),
     "gb_adamw_step": (_I, [_P, _P, _P]),
+    "gb_layer_norm_forward": (_I, [_I, _P, _S, _P, _S, _S, _S, _I, _P, _P, _D, _P, _P, _P]),
+    "gb_layer_norm_workspace_bytes": (_S, [_S, _S]),
+    "gb_layer_norm_backward": (_I, [_I, _P, _S, _P, _S, _P, _S, _S, _S, _P, _P, _I, _P, _I, _P, _P, _I, _P, _S, _P]),
+    "gb_embedding_forward": (_I, [_I, _P, _S, _I, _P, _S, _S, _S, _I, _P, _S, _L, _D, _P]),
+    "gb_embedding_workspace_bytes": (_S, [_S, _S, _S]),
+    "gb_embedding_backward": (_I, [_I, _P, _S, _S, _S, _I, _P, _S, _I, _P, _S, _L, _L, _D, _I, _P, _S, _P]),
     "gb_payload_bytes": (_S, [_I, _S]),
     "gb_bucket_workspace_layout": (_I, [_I, _I, _S, _S, _SP, _SP, _SP, _SP]),
     "gb_bucket_workspace_bytes": (_S, [_I, _I, _S, _S]),
@@ -695,6 +705,177 @@ def gb_optim_begin_clip(plan, control, max_norm, inv_scale=1.0, stream=None):
 def gb_adamw_step(plan, control, stream=None):
     """The AdamW update of every tensor of the plan, for the step last opened."""
     _check(_lib.gb_adamw_step(plan.ref, _control(control, plan), _plan_stream(plan, stream)))
+
+
+_LAYER_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_ID_TYPES = {torch.int32: 6, torch.int64: 7}
+
+
+def _layer_tensor(t, device, name, types=_LAYER_TYPES):
+    """gb_dtype number of a device tensor of one of types, on device if given."""
+    if isinstance(t, torch.Tensor):
+        number = types.get(t.dtype)
+        if number is not None and t.is_cuda and (device is None or t.get_device() == device):
+            return number
+        if number is None:
+            raise TypeError(f"{name} must be a tensor of one of {list(types)}, not {t.dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be in device memory, not on {t.device}")
+        raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{device}")
+    raise TypeError(f"{name} must be a torch.Tensor")
+
+
+def _matrix(t, name):
+    """(rows, cols, stride) of a 2-D tensor of unit stride along its rows, or of
+    a contiguous tensor of any other shape, its last dimension the row."""
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        stride, unit = t.stride()
+        if unit == 1 or cols <= 1:
+            return rows, cols, stride
+    elif len(shape) > 0 and t.is_contiguous():
+        cols = shape[-1]
+        return (t.numel() // cols if cols else 0), cols, cols
+    raise ValueError(f"{name} must be 2-D with adjacent values in a row, or contiguous")
+
+
+def _layer_matrix(t, device, name, dtype, rows, cols):
+    """(address, stride) of a rows x cols matrix of dtype."""
+    _layer_tensor(t, device, name)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    r, c, stride = _matrix(t, name)
+    if r != rows or c != cols:
+        raise ValueError(f"{name} has {r} rows of {c} values, expected {rows} of {cols}")
+    return t.data_ptr(), stride
+
+
+def _layer_vector(t, device, name, n, types=_LAYER_TYPES):
+    """(address, gb_dtype) of a contiguous tensor of n values, or (None, None)."""
+    if t is None:
+        return None, None
+    number = _layer_tensor(t, device, name, types)
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), number
+
+
+def _layer_pair(a, b, device, names, n):
+    """Addresses of two vectors that share one element type, and its number
+    (float32's without either)."""
+    pa, ta = _layer_vector(a, device, names[0], n)
+    pb, tb = _layer_vector(b, device, names[1], n)
+    if ta is not None and tb is not None and ta != tb:
+        raise TypeError(f"{names[1]} must be {a.dtype} as {names[0]} is, not {b.dtype}")
+    return pa, pb, ta if ta is not None else tb if tb is not None else 0
+
+
+def _layer_workspace(workspace, device):
+    if workspace is None:
+        return None, 0
+    return _layer_vector(workspace, device, "workspace", workspace.numel(), _BYTES)[0], workspace.numel()
+
+
+_F32, _BYTES = {torch.float32: 0}, {torch.uint8: 5}
+
+
+def _layer_call(name, device, stream, *args):
+    """One library call on the device's current stream, or the one given, with
+    the device current: the null stream's handle names no device."""
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(device)
+    else:
+        handle = torch.cuda.current_stream(device).cuda_stream
+    call = getattr(_lib, name)
+    if torch.cuda.current_device() == device:
+        status = call(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = call(*args, handle)
+    if status != GB_OK:
+        raise GbError(status, gb_last_error())
+
+
+def gb_layer_norm_forward(y, x, weight=None, bias=None, eps=1e-5, mean=None, rstd=None, stream=None):
+    """y = (x - mean) * rstd * weight + bias over the rows of x (float32,
+    float16 or bfloat16; y shares the type and may be x): 2-D with adjacent
+    values in a row, or contiguous with the last dimension the row.  weight and
+    bias share a type of their own; mean and rstd (float32, one value a row)
+    receive the statistics that gb_layer_norm_backward reads."""
+    dtype = _layer_tensor(x, None, "x")
+    device = x.get_device()
+    rows, cols, x_stride = _matrix(x, "x")
+    y_ptr, y_stride = _layer_matrix(y, device, "y", x.dtype, rows, cols)
+    w, b, param = _layer_pair(weight, bias, device, ("weight", "bias"), cols)
+    _layer_call("gb_layer_norm_forward", device, stream, dtype, y_ptr, y_stride, x.data_ptr(), x_stride, rows, cols,
+                param, w, b, eps, _layer_vector(mean, device, "mean", rows, _F32)[0],
+                _layer_vector(rstd, device, "rstd", rows, _F32)[0])
+
+
+def gb_layer_norm_workspace_bytes(rows, cols):
+    """Workspace bytes of gb_layer_norm_backward with dweight or dbias."""
+    return int(_lib.gb_layer_norm_workspace_bytes(int(rows), int(cols)))
+
+
+def gb_layer_norm_backward(dx, dweight, dbias, dy, x, mean, rstd, weight=None, accumulate=False, workspace=None,
+                           stream=None):
+    """The gradients of gb_layer_norm_forward from dy: dx (x's type; may be dy
+    or x; None: not computed), and the sums over all rows dweight and dbias (a
+    type of their own, or None), added to what they hold with accumulate.
+    workspace: a uint8 tensor of gb_layer_norm_workspace_bytes(rows, cols)."""
+    dtype = _layer_tensor(x, None, "x")
+    device = x.get_device()
+    rows, cols, x_stride = _matrix(x, "x")
+    dy_ptr, dy_stride = _layer_matrix(dy, device, "dy", x.dtype, rows, cols)
+    dx_ptr, dx_stride = (None, 0) if dx is None else _layer_matrix(dx, device, "dx", x.dtype, rows, cols)
+    dw, db, grad = _layer_pair(dweight, dbias, device, ("dweight", "dbias"), cols)
+    w, param = _layer_vector(weight, device, "weight", cols)
+    _layer_call("gb_layer_norm_backward", device, stream, dtype, dx_ptr, dx_stride, dy_ptr, dy_stride, x.data_ptr(),
+                x_stride, rows, cols, _layer_vector(mean, device, "mean", rows, _F32)[0],
+                _layer_vector(rstd, device, "rstd", rows, _F32)[0], param or 0, w, grad, dw, db,
+                1 if accumulate else 0, *_layer_workspace(workspace, device))
+
+
+def gb_embedding_forward(out, table, ids, scale=1.0, first=0, stream=None):
+    """out[t] = scale * table[ids[t] - first], zeros where that is no row of
+    the table: first is the first id of a shard of the vocabulary.  out and
+    table are float32, float16 or bfloat16 each, ids int32 or int64."""
+    table_type = _layer_tensor(table, None, "table")
+    device = table.get_device()
+    vocab, dim, table_stride = _matrix(table, "table")
+    ids_ptr, id_type = _layer_vector(ids, device, "ids", ids.numel() if isinstance(ids, torch.Tensor) else 0, _ID_TYPES)
+    out_type = _layer_tensor(out, device, "out")
+    out_ptr, out_stride = _layer_matrix(out, device, "out", out.dtype, ids.numel(), dim)
+    _layer_call("gb_embedding_forward", device, stream, out_type, out_ptr, out_stride, table_type, table.data_ptr(),
+                table_stride, vocab, dim, id_type, ids_ptr, ids.numel(), first, scale)
+
+
+def gb_embedding_workspace_bytes(tokens, vocab, dim):
+    """Workspace bytes of gb_embedding_backward."""
+    return int(_lib.gb_embedding_workspace_bytes(int(tokens), int(vocab), int(dim)))
+
+
+def gb_embedding_backward(dtable, dout, ids, scale=1.0, first=0, padding=-1, accumulate=False, workspace=None,
+                          stream=None):
+    """The table's gradient of gb_embedding_forward: each row of dtable is
+    scale times the sum of dout over the tokens with its id, added to what the
+    row holds with accumulate; ids equal to padding, or outside the table,
+    count nowhere.  dtable and dout are float32, float16 or bfloat16 each.
+    workspace: a uint8 tensor of gb_embedding_workspace_bytes(...) bytes."""
+    grad_type = _layer_tensor(dtable, None, "dtable")
+    device = dtable.get_device()
+    vocab, dim, dtable_stride = _matrix(dtable, "dtable")
+    ids_ptr, id_type = _layer_vector(ids, device, "ids", ids.numel() if isinstance(ids, torch.Tensor) else 0, _ID_TYPES)
+    dtype = _layer_tensor(dout, device, "dout")
+    dout_ptr, dout_stride = _layer_matrix(dout, device, "dout", dout.dtype, ids.numel(), dim)
+    _layer_call("gb_embedding_backward", device, stream, grad_type, dtable.data_ptr(), dtable_stride, vocab, dim,
+                dtype, dout_ptr, dout_stride, id_type, ids_ptr, ids.numel(), first, padding, scale,
+                1 if accumulate else 0, *_layer_workspace(workspace, device))
 
 
 def gb_payload_bytes(codec, n):

@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgbreduce.so")
 # The kernels are split over several sources so that they compile in parallel.
 SOURCES = ["gb_reduce.hip", "gb_codec_fp8.hip", "gb_codec_bf16.hip", "gb_ef.hip", "gb_noalloc.hip",
-           "gb_optim.hip", "gb_api.cpp", "gb_optim_api.cpp"]
+           "gb_optim.hip", "gb_norm.hip", "gb_embed.hip", "gb_api.cpp", "gb_optim_api.cpp", "gb_layers_api.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # The memory-ceiling measurement program bench.py runs (not part of the library).
 CEILING_SRC = "gb_ceiling.hip"

@@ -18,8 +18,10 @@
  * and, around them: AVG, MAX and MIN; the README's other element types,
  * reduced exactly or through the codecs; an error-feedback residual per
  * buffer; the bucket stream over buckets held in separate buffers, several
- * per launch; the staged (pipelined) steps through pinned host memory; and
- * the optimizer's step on the reduced gradients (norm, clipping, AdamW).
+ * per launch; the staged (pipelined) steps through pinned host memory; the
+ * optimizer's step on the reduced gradients (norm, clipping, AdamW); and the
+ * layers whose parameters' gradients are sums over tokens (layer norm and the
+ * embedding table), which leave them in the buckets.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -730,6 +732,119 @@ gb_status gb_optim_begin_clip(const gb_optim_handle* plan, void* control, double
  * call on this control block opened.  One launch for each combination of
  * gradient type and state that the plan holds (and for each 2^33 values). */
 gb_status gb_adamw_step(const gb_optim_handle* plan, const void* control, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The layers whose parameters' gradients are sums over tokens: layer norm and
+ * the embedding table, forward and backward.  (The pages begin with full
+ * gradient buckets; matrix products write theirs there by themselves, and
+ * these calls add the two sums: over all rows for a layer norm's weight and
+ * bias, over the tokens of each id for the table.)  A gradient goes straight
+ * to its place in a bucket, written or, for the later micro-batches of a step,
+ * added (accumulate); every sum has an order that sizes and ids fix, so a
+ * result is bit-reproducible.
+ *
+ * 2-D arrays: unit stride along a row, `stride` elements from row to row, for
+ * an output at least the row's length (an input's rows may overlap, or repeat
+ * with a stride of 0; looked at only where there are several rows).  They
+ * and the parameters and gradients need only the alignment of their element:
+ * all may be views.  For the overlap rule an array reaches from its first
+ * value to its last, the gaps between its rows included.  Types are
+ * GB_DTYPE_F32, F16 or BF16 each; arithmetic is binary32, and an output is
+ * rounded to its type once.  Every NaN is stored as 0x7FC00000, or as that
+ * NaN's rounding.  Calls with different workspaces may run at the same time;
+ * two that share one belong on one stream, or ordered by events.
+ * ------------------------------------------------------------------------- */
+
+/* Longest row of the layer norm calls. */
+#define GB_NORM_MAX_COLS 32768
+
+/*
+ * gb_layer_norm_forward — for each of `rows` rows of `cols` values:
+ *   mean = (sum of x) / cols
+ *   rstd = 1 / sqrt((sum of (x - mean)^2) / cols + eps)
+ *   y = (x - mean) * rstd * weight + bias
+ *   y, x        dtype; y may be x (the same address and stride)
+ *   weight, bias  cols values of param_dtype; NULL is ones, zeros
+ *   mean, rstd  float[rows], written for the backward pass; NULL: not stored
+ * cols 1 .. GB_NORM_MAX_COLS; eps finite and above 0 in binary32.  rows == 0
+ * is GB_OK and enqueues nothing.  Forward and backward results agree with the
+ * formulas up to the binary32 roundings of their sums (not fixed bit for bit
+ * across versions of this library, as the codecs are).
+ */
+gb_status gb_layer_norm_forward(int dtype, void* y, size_t y_stride, const void* x, size_t x_stride, size_t rows,
+                                size_t cols, int param_dtype, const void* weight, const void* bias, double eps,
+                                float* mean, float* rstd, void* stream);
+
+/* Workspace bytes of gb_layer_norm_backward with dweight or dbias; 0 for no
+ * rows and for arguments it would refuse.  Host only. */
+size_t gb_layer_norm_workspace_bytes(size_t rows, size_t cols);
+
+/*
+ * gb_layer_norm_backward — the gradients, from dy (that of y), x and the
+ * statistics the forward pass stored.  With h = (x - mean) * rstd and
+ * g = dy * weight:
+ *   dx = rstd * (g - (sum of g) / cols - h * (sum of g * h) / cols)
+ *   dweight = [dweight +] sum over the rows of dy * h
+ *   dbias   = [dbias +] sum over the rows of dy
+ * the terms in brackets with accumulate == 1.
+ *   dx       dtype, or NULL: not computed; may be dy or x (the same address
+ *            and stride)
+ *   dweight, dbias  cols values of grad_dtype, or NULL: not computed
+ *   weight   cols values of param_dtype; NULL is ones
+ *   workspace  16-byte aligned, not looked at without dweight and dbias
+ * rows == 0 writes zeros to dweight and dbias unless accumulate is set.  dx,
+ * dweight and dbias all NULL is GB_ERR_INVALID_ARG.
+ */
+gb_status gb_layer_norm_backward(int dtype, void* dx, size_t dx_stride, const void* dy, size_t dy_stride,
+                                 const void* x, size_t x_stride, size_t rows, size_t cols, const float* mean,
+                                 const float* rstd, int param_dtype, const void* weight, int grad_dtype,
+                                 void* dweight, void* dbias, int accumulate, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Most tokens of an embedding call, rows of its table, and values of a row. */
+#define GB_EMBEDDING_MAX_TOKENS (1 << 30)
+#define GB_EMBEDDING_MAX_VOCAB 2147483647
+#define GB_EMBEDDING_MAX_DIM (1 << 20)
+
+/*
+ * gb_embedding_forward — for each token t with r = ids[t] - first:
+ *   out[t][i] = RN(scale * table[r][i])   where 0 <= r < vocab
+ *             = 0                         elsewhere
+ * `first` is the first id of a shard of the vocabulary (0 for a whole table):
+ * every shard's call gives zeros for the other shards' tokens, so the sum of
+ * the shards' outputs holds every token's row.  Ids may hold any value; first +
+ * vocab is at most 2^63 - 1.
+ *   out    tokens x dim of out_dtype;  table  vocab x dim of table_dtype
+ *   ids    int32 or int64 (id_dtype GB_DTYPE_I32 or I64)
+ *   scale  finite in binary32, rounded to it
+ */
+gb_status gb_embedding_forward(int out_dtype, void* out, size_t out_stride, int table_dtype, const void* table,
+                               size_t table_stride, size_t vocab, size_t dim, int id_dtype, const void* ids,
+                               size_t tokens, int64_t first, double scale, void* stream);
+
+/* Workspace bytes of gb_embedding_backward; 0 where it needs none (no tokens,
+ * no rows, empty rows) and for arguments it would refuse.  Host only. */
+size_t gb_embedding_workspace_bytes(size_t tokens, size_t vocab, size_t dim);
+
+/*
+ * gb_embedding_backward — the table's gradient, from dout (that of out):
+ *   dtable[r][i] = [dtable[r][i] +] RN(scale * S(dout[t][i] over the tokens t with ids[t] - first == r))
+ * the term in brackets with accumulate == 1.  A token whose id is `padding`
+ * (-1: none, where no id is) or outside the shard is left out.  Without
+ * accumulate every row is written, those without a token with zeros; with it
+ * only the rows that tokens name are read and written.
+ * S adds in binary32 in the order of the tokens, 64 at a time: the first 64
+ * in turn, the next 64, and so on; those sums again 64 at a time, until one is left.
+ *   dtable  vocab x dim of grad_dtype;  dout  tokens x dim of dtype
+ *   workspace  16-byte aligned
+ * The tokens are sorted by row (a stable radix sort), and each row's tokens
+ * are then added where they lie: dout is read once, dtable written once, and
+ * nothing is added by atomic operations.
+ */
+gb_status gb_embedding_backward(int grad_dtype, void* dtable, size_t dtable_stride, size_t vocab, size_t dim,
+                                int dtype, const void* dout, size_t dout_stride, int id_dtype, const void* ids,
+                                size_t tokens, int64_t first, int64_t padding, double scale, int accumulate,
+                                void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes one rank's n-value payload occupies on the bridge:
  * 4n (NONE), 2n (BF16), n + 4*ceil(n/256) (FP8).  0 for an unknown codec. */
