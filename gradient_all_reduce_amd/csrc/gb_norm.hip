@@ -13,11 +13,87 @@ namespace {
 // contiguous run.  Each value is read from memory once; mean and variance are
 // two passes over registers, so the variance is a sum of squared deviations
 // and loses nothing to cancellation.
+//
+// A vector that would pass the row's end is moved back to end with the row:
+// every load and store is a whole vector without a branch, the values it
+// shares with its neighbour (skip of them, all V in a lane beyond the row)
+// count in the neighbour's sums alone, and both store the same bits.  Rows
+// shorter than a vector (SHORT) are read value by value.
 // ---------------------------------------------------------------------------
-template <int ET, int L, int W, int K>
+template <int ET, int L, int W, int K, bool SHORT>
 struct Team {
-  static constexpr int kV = Type<ET>::kVec, kLanes = L * W, kCols = kLanes * K * kV;
+  static constexpr int V = Type<ET>::kVec, kLanes = L * W, kCols = kLanes * K * V;
+  uint32_t lane, at[K], skip[K], cols;
+  uint32_t last;  // of the wavefront's lanes in the team
+
+  __device__ __forceinline__ explicit Team(uint32_t n) : lane(threadIdx.x % kLanes), cols(n) {
+    last = L < kWave ? L - 1 : __builtin_amdgcn_readfirstlane(lane / kWave) * kWave + kWave - 1;
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      const uint32_t col = (k * kLanes + lane) * V;
+      at[k] = SHORT ? 0 : col + V <= n ? col : n - V;
+      skip[k] = SHORT ? (lane == 0 ? V - n : V) : col - at[k] < V ? col - at[k] : V;
+    }
+  }
+  // Whether vector k of some lane of the wavefront is not its own throughout.
+  __device__ __forceinline__ bool ragged(int k) const { return SHORT || (k * kLanes + last + 1) * V > cols; }
+  __device__ __forceinline__ bool mine(int k, int e) const {
+    return SHORT ? lane == 0 && e < (int)cols : e >= (int)skip[k];
+  }
+  __device__ __forceinline__ Raw<ET, V> load(const void* row, int k) const {
+    if constexpr (SHORT) return load_raw<ET, V, true>(row, 0u, lane == 0 ? cols : 0u);
+    else return load_full<ET, V, true>(row, at[k]);
+  }
+  __device__ __forceinline__ void store(void* row, int k, const float (&v)[V]) const {
+    if constexpr (SHORT) store_vals<ET, V, true>(row, 0u, lane == 0 ? cols : 0u, v);
+    else if (!ragged(k) || skip[k] < V) store_vals<ET, V, true>(row, at[k], V, v);
+  }
+  template <int PT>
+  __device__ __forceinline__ void param_of(float (&to)[V], const void* p, int k) const {
+    constexpr int P = Type<PT>::kVec < V ? Type<PT>::kVec : V;
+#pragma unroll
+    for (int j = 0; j < V; j += P) {
+      Raw<PT, P> r;
+      if constexpr (SHORT) r = load_raw<PT, P, false>(p, (uint32_t)j, lane == 0 && (int)cols > j ? cols - j : 0u);
+      else r = load_full<PT, P, false>(p, at[k] + j);
+#pragma unroll
+      for (int e = 0; e < P; e++) to[j + e] = raw_value<PT, P>(r, e);
+    }
+  }
+  // A parameter's values at the lane's columns; none where there is no array.
+  __device__ __forceinline__ void param(float (&to)[K][V], const void* p, int dtype, float none) const {
+    if (p == nullptr) {
+#pragma unroll
+      for (int k = 0; k < K; k++) {
+#pragma unroll
+        for (int e = 0; e < V; e++) to[k][e] = none;
+      }
+    } else if (dtype == GB_DTYPE_F32) {
+#pragma unroll
+      for (int k = 0; k < K; k++) param_of<GB_DTYPE_F32>(to[k], p, k);
+    } else if (dtype == GB_DTYPE_F16) {
+#pragma unroll
+      for (int k = 0; k < K; k++) param_of<GB_DTYPE_F16>(to[k], p, k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; k++) param_of<GB_DTYPE_BF16>(to[k], p, k);
+    }
+  }
 };
+
+// Row r of an array, or the last row for an r beyond it.  Where a wavefront
+// holds one row (L == 64) its address is a scalar.
+template <int ET, int L>
+__device__ __forceinline__ char* row_at(const Rows& a, size_t r) {
+  return static_cast<char*>(a.p) + r * a.stride * Type<ET>::kSize;
+}
+// The team's number in the workgroup.
+template <int L, int LANES>
+__device__ __forceinline__ uint32_t team_number() {
+  const uint32_t t = threadIdx.x / LANES;
+  return L < kWave ? t : __builtin_amdgcn_readfirstlane(t);
+}
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < __builtin_inff(); }
 
 // Sum over the team: over the lanes of a wavefront in registers, over
 // wavefronts through LDS.  part: W floats of this team.  One barrier if W > 1.
@@ -34,76 +110,89 @@ __device__ __forceinline__ float team_sum(float v, float* part) {
   return v;
 }
 
-template <int ET, int L, int W, int K, int THREADS>
+template <int ET, int L, int W, int K, int THREADS, bool SHORT>
 __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
-  using T = Team<ET, L, W, K>;
-  constexpr int V = T::kV, kTeams = THREADS / T::kLanes;
+  using T = Team<ET, L, W, K, SHORT>;
+  constexpr int V = T::V, kTeams = THREADS / T::kLanes;
   __shared__ float part[W > 1 ? 2 : 1][W > 1 ? kTeams * W : 1];
-  const uint32_t lane = threadIdx.x % T::kLanes, team = threadIdx.x / T::kLanes;
+  const T t(a.cols);
+  const uint32_t team = team_number<L, T::kLanes>();
   float* const sum_part = &part[0][W > 1 ? team * W : 0];
   float* const var_part = &part[W > 1 ? 1 : 0][W > 1 ? team * W : 0];
-  const float n = (float)a.cols;
-
-  float w[K][V], b[K][V];
-  auto param = [&](float (&to)[K][V], const void* p, float none) {
-#pragma unroll
-    for (int k = 0; k < K; k++) {
-      const uint32_t col = (k * T::kLanes + lane) * V;
-#pragma unroll
-      for (int e = 0; e < V; e++) to[k][e] = p != nullptr && col + e < a.cols ? load_any(p, a.param_dtype, col + e) : none;
-    }
-  };
-  param(w, a.w, 1.0f);
-  param(b, a.b, 0.0f);
+  const float inv_n = 1.0f / (float)a.cols;
 
   Raw<ET, V> x[K];
   auto load_row = [&](size_t r) {
-    const size_t at = r * a.x.stride;
+    const void* const row = row_at<ET, L>(a.x, r < a.rows ? r : a.rows - 1);
 #pragma unroll
-    for (int k = 0; k < K; k++) {
-      const uint32_t col = (k * T::kLanes + lane) * V;
-      x[k] = r < a.rows ? load_raw<ET, V, true>(a.x.p, at + col, left_of(col, a.cols)) : zero_raw<ET, V>();
-    }
+    for (int k = 0; k < K; k++) x[k] = t.load(row, k);
   };
-  const size_t step = (size_t)gridDim.x * kTeams;
-  // the same number of rounds in every team of the workgroup: they meet at barriers
-  const size_t first = (size_t)blockIdx.x * kTeams;
+  const size_t step = (size_t)gridDim.x * kTeams, first = (size_t)blockIdx.x * kTeams;
   load_row(first + team);
+  float w[K][V], b[K][V];
+  t.param(w, a.w, a.param_dtype, 1.0f);
+  t.param(b, a.b, a.param_dtype, 0.0f);
+  bool plain = true;  // the lane's parameters are finite
+#pragma unroll
+  for (int k = 0; k < K; k++) {
+#pragma unroll
+    for (int e = 0; e < V; e++) plain = plain && finite(w[k][e]) && finite(b[k][e]);
+  }
+  // the same number of rounds in every team of the workgroup: they meet at barriers
   for (size_t base = first; base < a.rows; base += step) {
     const size_t r = base + team;
     float v[K][V], sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; k++) {
 #pragma unroll
-      for (int e = 0; e < V; e++) {
-        v[k][e] = raw_value<ET, V>(x[k], e);  // zeros beyond the row
-        sum += v[k][e];
+      for (int e = 0; e < V; e++) v[k][e] = raw_value<ET, V>(x[k], e);
+      if (t.ragged(k)) {
+#pragma unroll
+        for (int e = 0; e < V; e++) sum += t.mine(k, e) ? v[k][e] : 0.0f;
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; e++) sum += v[k][e];
       }
     }
     if (base + step < a.rows) load_row(r + step);
-    const float mean = team_sum<L, W>(sum, sum_part) / n;
+    const float mean = team_sum<L, W>(sum, sum_part) * inv_n;
     float square = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; k++) {
-      const uint32_t left = left_of((k * T::kLanes + lane) * V, a.cols);
 #pragma unroll
-      for (int e = 0; e < V; e++) {
-        v[k][e] = left >= V || e < (int)left ? v[k][e] - mean : 0.0f;
-        square = fmaf(v[k][e], v[k][e], square);
+      for (int e = 0; e < V; e++) v[k][e] -= mean;
+      if (t.ragged(k)) {
+#pragma unroll
+        for (int e = 0; e < V; e++) square = t.mine(k, e) ? fmaf(v[k][e], v[k][e], square) : square;
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; e++) square = fmaf(v[k][e], v[k][e], square);
       }
     }
-    const float rstd = 1.0f / sqrtf(team_sum<L, W>(square, var_part) / n + a.eps);
+    const float rstd = 1.0f / sqrtf(team_sum<L, W>(square, var_part) * inv_n + a.eps);
     if (r < a.rows) {
-      const size_t at = r * a.y.stride;
+      void* const row = row_at<ET, L>(a.y, r);
+      // With mean, rstd, weight and bias finite no value is NaN: a deviation
+      // times rstd is at most the root of cols, and a fused product and sum of
+      // finite numbers may overflow but has a sign.
+      if (__all(plain && finite(mean) && finite(rstd))) {
 #pragma unroll
-      for (int k = 0; k < K; k++) {
-        const uint32_t col = (k * T::kLanes + lane) * V;
-        float y[V];
+        for (int k = 0; k < K; k++) {
+          float y[V];
 #pragma unroll
-        for (int e = 0; e < V; e++) y[e] = canon(fmaf(v[k][e] * rstd, w[k][e], b[k][e]));
-        store_vals<ET, V, true>(a.y.p, at + col, left_of(col, a.cols), y);
+          for (int e = 0; e < V; e++) y[e] = fmaf(v[k][e] * rstd, w[k][e], b[k][e]);
+          t.store(row, k, y);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+          float y[V];
+#pragma unroll
+          for (int e = 0; e < V; e++) y[e] = canon(fmaf(v[k][e] * rstd, w[k][e], b[k][e]));
+          t.store(row, k, y);
+        }
       }
-      if (lane == 0) {
+      if (t.lane == 0) {
         if (a.mean != nullptr) a.mean[r] = canon(mean);
         if (a.rstd != nullptr) a.rstd[r] = canon(rstd);
       }
@@ -117,60 +206,93 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
 // row to the last, so the weight's gradient costs no traffic until the end,
 // when the workgroup leaves one row of partial sums for each.
 // ---------------------------------------------------------------------------
-template <int ET, int L, int W, int K, int THREADS>
+template <int ET, int L, int W, int K, int THREADS, bool SHORT>
 __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
-  using T = Team<ET, L, W, K>;
-  constexpr int V = T::kV, kTeams = THREADS / T::kLanes;
+  using T = Team<ET, L, W, K, SHORT>;
+  constexpr int V = T::V, kTeams = THREADS / T::kLanes;
+  // h and g stay in registers between the two passes over a row, or are
+  // worked out again from the row's values
+  constexpr bool kKeep = K * V <= 16;
+  // the next row is read ahead while the registers hold it
+  constexpr bool kAhead = K <= 4;
   __shared__ float part[2][2][W > 1 ? kTeams * W : 1];
-  const uint32_t lane = threadIdx.x % T::kLanes, team = threadIdx.x / T::kLanes;
+  const T t(a.cols);
+  const uint32_t team = team_number<L, T::kLanes>();
   const float inv_n = 1.0f / (float)a.cols;
 
-  float w[K][V], dw[K][V], db[K][V];
-#pragma unroll
-  for (int k = 0; k < K; k++) {
-    const uint32_t col = (k * T::kLanes + lane) * V;
-#pragma unroll
-    for (int e = 0; e < V; e++) {
-      w[k][e] = a.w != nullptr && col + e < a.cols ? load_any(a.w, a.param_dtype, col + e) : 1.0f;
-      dw[k][e] = db[k][e] = 0.0f;
-    }
-  }
   Raw<ET, V> x[K], dy[K];
   float mean, rstd;
   auto load_row = [&](size_t r) {
-    const bool in = r < a.rows;
+    r = r < a.rows ? r : a.rows - 1;
+    const void *const x_row = row_at<ET, L>(a.x, r), *const dy_row = row_at<ET, L>(a.dy, r);
 #pragma unroll
     for (int k = 0; k < K; k++) {
-      const uint32_t col = (k * T::kLanes + lane) * V;
-      x[k] = in ? load_raw<ET, V, true>(a.x.p, r * a.x.stride + col, left_of(col, a.cols)) : zero_raw<ET, V>();
-      dy[k] = in ? load_raw<ET, V, true>(a.dy.p, r * a.dy.stride + col, left_of(col, a.cols)) : zero_raw<ET, V>();
+      x[k] = t.load(x_row, k);
+      dy[k] = t.load(dy_row, k);
     }
-    mean = in ? a.mean[r] : 0.0f;
-    rstd = in ? a.rstd[r] : 0.0f;
+    mean = a.mean[r];
+    rstd = a.rstd[r];
   };
   const size_t step = (size_t)gridDim.x * kTeams, first = (size_t)blockIdx.x * kTeams;
   load_row(first + team);
+  float w[K][V], dw[K][V], db[K][V];
+  t.param(w, a.w, a.param_dtype, 1.0f);
+#pragma unroll
+  for (int k = 0; k < K; k++) {
+#pragma unroll
+    for (int e = 0; e < V; e++) dw[k][e] = db[k][e] = 0.0f;
+  }
   int parity = 0;
   for (size_t base = first; base < a.rows; base += step, parity ^= 1) {
     const size_t r = base + team;
-    float h[K][V], g[K][V], c1 = 0.0f, c2 = 0.0f;
+    if (!kAhead && base != first) load_row(r);
+    if (base + kTeams > a.rows && r >= a.rows) {  // a team without a row adds nothing
+#pragma unroll
+      for (int k = 0; k < K; k++) x[k] = dy[k] = zero_raw<ET, V>();
+      mean = rstd = 0.0f;
+    }
+    float h[kKeep ? K : 1][V], g[kKeep ? K : 1][V], c1 = 0.0f, c2 = 0.0f;
     const float m = mean, s = rstd;
+    Raw<ET, V> x_now[K], dy_now[K];
 #pragma unroll
     for (int k = 0; k < K; k++) {
-      const uint32_t left = left_of((k * T::kLanes + lane) * V, a.cols);
+      x_now[k] = x[k];
+      dy_now[k] = dy[k];
+    }
+    auto terms = [&](int k, float (&hk)[V], float (&gk)[V]) {
 #pragma unroll
       for (int e = 0; e < V; e++) {
-        const float d = raw_value<ET, V>(dy[k], e);
-        // beyond the row d is 0 but the mean need not be, and 0 * Inf is NaN
-        h[k][e] = left >= V || e < (int)left ? (raw_value<ET, V>(x[k], e) - m) * s : 0.0f;
-        g[k][e] = d * w[k][e];
-        c1 += g[k][e];
-        c2 = fmaf(g[k][e], h[k][e], c2);
-        dw[k][e] = fmaf(d, h[k][e], dw[k][e]);
+        hk[e] = (raw_value<ET, V>(x_now[k], e) - m) * s;
+        gk[e] = raw_value<ET, V>(dy_now[k], e) * w[k][e];
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      float(&hk)[V] = h[kKeep ? k : 0];
+      float(&gk)[V] = g[kKeep ? k : 0];
+      if constexpr (!kKeep) __builtin_amdgcn_sched_barrier(0);
+      terms(k, hk, gk);
+#pragma unroll
+      for (int e = 0; e < V; e++) {
+        const float d = raw_value<ET, V>(dy_now[k], e);
+        dw[k][e] = fmaf(d, hk[e], dw[k][e]);
         db[k][e] += d;
       }
+      if (t.ragged(k)) {
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+          c1 += t.mine(k, e) ? gk[e] : 0.0f;
+          c2 = t.mine(k, e) ? fmaf(gk[e], hk[e], c2) : c2;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+          c1 += gk[e];
+          c2 = fmaf(gk[e], hk[e], c2);
+        }
+      }
     }
-    if (base + step < a.rows) load_row(r + step);
+    if (kAhead && base + step < a.rows) load_row(r + step);
     if (a.dx.p == nullptr) continue;
     c1 = lanes_sum<L>(c1);
     c2 = lanes_sum<L>(c2);
@@ -191,15 +313,36 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
     }
     c1 *= inv_n * s;
     c2 *= inv_n * s;
-    if (r < a.rows) {
-      const size_t at = r * a.dx.stride;
+    if constexpr (!kKeep) {
+      // or the compiler keeps h and g after all, and spills them
 #pragma unroll
       for (int k = 0; k < K; k++) {
-        const uint32_t col = (k * T::kLanes + lane) * V;
+#pragma unroll
+        for (int j = 0; j < 4; j++) asm volatile("" : "+v"(x_now[k].w[j]), "+v"(dy_now[k].w[j]));
+      }
+    }
+    if (r < a.rows) {
+      void* const row = row_at<ET, L>(a.dx, r);
+      // With both sums and rstd finite so are all g and h (an infinite one
+      // would show in a sum), and fused products and sums of finite numbers
+      // may overflow but have a sign: no value is NaN.
+      const bool plain = __all(finite(c1) && finite(c2) && finite(s));
+#pragma unroll
+      for (int k = 0; k < K; k++) {
+        float(&hk)[V] = h[kKeep ? k : 0];
+        float(&gk)[V] = g[kKeep ? k : 0];
+        if constexpr (!kKeep) {
+          __builtin_amdgcn_sched_barrier(0);
+          terms(k, hk, gk);
+        }
         float dx[V];
 #pragma unroll
-        for (int e = 0; e < V; e++) dx[e] = canon(fmaf(-h[k][e], c2, fmaf(g[k][e], s, -c1)));
-        store_vals<ET, V, true>(a.dx.p, at + col, left_of(col, a.cols), dx);
+        for (int e = 0; e < V; e++) dx[e] = fmaf(-hk[e], c2, fmaf(gk[e], s, -c1));
+        if (!plain) {
+#pragma unroll
+          for (int e = 0; e < V; e++) dx[e] = canon(dx[e]);
+        }
+        t.store(row, k, dx);
       }
     }
   }
@@ -219,21 +362,21 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
       }
     }
   }
-  const size_t stride = a.partial_stride;
-  float* const out = a.partials + (size_t)blockIdx.x * 2 * stride;
+  float* const out = a.partials + (size_t)blockIdx.x * 2 * a.partial_stride;
   constexpr int kJoin = L < kWave ? THREADS / kWave : kTeams;  // sums left to join
-  if constexpr (kJoin > 1) {
+  if constexpr (kJoin > 1 || SHORT) {
     __shared__ float joined[2][T::kCols];
     const uint32_t mine = L < kWave ? threadIdx.x / kWave : team;
     for (uint32_t j = 0; j < kJoin; j++) {
       if (mine == j && (L == kWave || threadIdx.x % kWave < L)) {
 #pragma unroll
         for (int k = 0; k < K; k++) {
-          const uint32_t col = (k * T::kLanes + lane) * V;
 #pragma unroll
           for (int e = 0; e < V; e++) {
-            joined[0][col + e] = j == 0 ? dw[k][e] : joined[0][col + e] + dw[k][e];
-            joined[1][col + e] = j == 0 ? db[k][e] : joined[1][col + e] + db[k][e];
+            if (!t.mine(k, e)) continue;
+            const uint32_t c = t.at[k] + e;
+            joined[0][c] = j == 0 ? dw[k][e] : joined[0][c] + dw[k][e];
+            joined[1][c] = j == 0 ? db[k][e] : joined[1][c] + db[k][e];
           }
         }
       }
@@ -241,19 +384,18 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
     }
     for (uint32_t c = threadIdx.x; c < a.cols; c += THREADS) {
       if (a.dw != nullptr) out[c] = joined[0][c];
-      if (a.db != nullptr) out[stride + c] = joined[1][c];
+      if (a.db != nullptr) out[a.partial_stride + c] = joined[1][c];
     }
   } else {
 #pragma unroll
     for (int k = 0; k < K; k++) {
-      const uint32_t col = (k * T::kLanes + lane) * V, left = left_of(col, a.cols);
+      if (t.skip[k] >= V) continue;
 #pragma unroll
       for (int j = 0; j < V; j += 4) {
-        const uint32_t l = left > (uint32_t)j ? left - j : 0u;
         const float pw[4] = {dw[k][j], dw[k][j + 1], dw[k][j + 2], dw[k][j + 3]};
         const float pb[4] = {db[k][j], db[k][j + 1], db[k][j + 2], db[k][j + 3]};
-        if (a.dw != nullptr) store_vals<GB_DTYPE_F32, 4, false>(out, col + j, l, pw);
-        if (a.db != nullptr) store_vals<GB_DTYPE_F32, 4, false>(out, stride + col + j, l, pb);
+        if (a.dw != nullptr) store_vals<GB_DTYPE_F32, 4, false>(out, t.at[k] + j, 4, pw);
+        if (a.db != nullptr) store_vals<GB_DTYPE_F32, 4, false>(out, a.partial_stride + t.at[k] + j, 4, pb);
       }
     }
   }
@@ -296,18 +438,19 @@ __global__ __launch_bounds__(kJoinLanes* kSlices) void norm_join_kernel(NormGrad
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-template <int ET, int L, int W, int K>
+template <int ET, int L, int W, int K, bool SHORT = false>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
   constexpr int kThreads = W > 4 ? W * kWave : 256;
   constexpr size_t kTeams = kThreads / (L * W);
   size_t grid = (a.rows + kTeams - 1) / kTeams;
   if (grid > 2048) grid = 2048;
-  norm_kernel<ET, L, W, K, kThreads><<<dim3((unsigned)grid), dim3(kThreads), 0, stream>>>(a);
+  norm_kernel<ET, L, W, K, kThreads, SHORT><<<dim3((unsigned)grid), dim3(kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <int ET>
 hipError_t pick_norm(const NormArgs& a, hipStream_t stream) {
   const uint32_t v = (a.cols + Type<ET>::kVec - 1) / Type<ET>::kVec;
+  if (a.cols < Type<ET>::kVec) return run_norm<ET, 8, 1, 1, true>(a, stream);
   if (v <= 8) return run_norm<ET, 8, 1, 1>(a, stream);
   if (v <= 16) return run_norm<ET, 16, 1, 1>(a, stream);
   if (v <= 32) return run_norm<ET, 32, 1, 1>(a, stream);
@@ -323,7 +466,7 @@ hipError_t pick_norm(const NormArgs& a, hipStream_t stream) {
   return run_norm<ET, 64, 16, 4>(a, stream);
 }
 
-template <int ET, int L, int W, int K>
+template <int ET, int L, int W, int K, bool SHORT = false>
 struct NormGrad {
   static constexpr int kThreads = W > 4 ? W * kWave : 256;
   static constexpr size_t kTeams = kThreads / (L * W);
@@ -333,7 +476,7 @@ struct NormGrad {
   }
   static hipError_t run(const NormGradArgs& a, hipStream_t stream) {
     const uint32_t g = groups(a.rows, a.cols);
-    if (g > 0) norm_grad_kernel<ET, L, W, K, kThreads><<<dim3(g), dim3(kThreads), 0, stream>>>(a);
+    if (g > 0) norm_grad_kernel<ET, L, W, K, kThreads, SHORT><<<dim3(g), dim3(kThreads), 0, stream>>>(a);
     return hipGetLastError();
   }
 };
@@ -341,6 +484,7 @@ struct NormGrad {
 template <int ET, class F>
 auto with_norm_grad(size_t cols, F&& f) {
   const size_t v = (cols + Type<ET>::kVec - 1) / Type<ET>::kVec;
+  if (cols < Type<ET>::kVec) return f(NormGrad<ET, 8, 1, 1, true>());
   if (v <= 8) return f(NormGrad<ET, 8, 1, 1>());
   if (v <= 16) return f(NormGrad<ET, 16, 1, 1>());
   if (v <= 32) return f(NormGrad<ET, 32, 1, 1>());

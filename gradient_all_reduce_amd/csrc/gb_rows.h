@@ -89,19 +89,29 @@ struct Raw {
   static constexpr int kWords = V * Type<ET>::kSize / 4;
   uint32_t w[kWords];
 };
-template <int ET, int V, bool NT>
-__device__ __forceinline__ Raw<ET, V> load_full(const void* p, size_t i) {
+// The address of value i.  Of 32 bits, i is a lane's offset from an address
+// that the wavefront shares, which the load or store instruction adds itself.
+template <int ET, class I>
+__device__ __forceinline__ const GB_GLOBAL char* value_at(const void* p, I i) {
+  return (const GB_GLOBAL char*)p + (I)(i * Type<ET>::kSize);
+}
+template <int ET, class I>
+__device__ __forceinline__ GB_GLOBAL char* value_at(void* p, I i) {
+  return (GB_GLOBAL char*)p + (I)(i * Type<ET>::kSize);
+}
+template <int ET, int V, bool NT, class I>
+__device__ __forceinline__ Raw<ET, V> load_full(const void* p, I i) {
   Raw<ET, V> r;
   if constexpr (Type<ET>::kSize == 4) {
     static_assert(V == 4, "");
-    const GB_GLOBAL u4_any4* q = (const GB_GLOBAL u4_any4*)((const GB_GLOBAL uint32_t*)p + i);
+    const GB_GLOBAL u4_any4* q = (const GB_GLOBAL u4_any4*)value_at<ET>(p, i);
     u4 v;
     if constexpr (NT) v = __builtin_nontemporal_load(q);
     else v = *q;
 #pragma unroll
     for (int j = 0; j < 4; j++) r.w[j] = v[j];
   } else if constexpr (V == 8) {
-    const GB_GLOBAL u4_any2* q = (const GB_GLOBAL u4_any2*)((const GB_GLOBAL uint16_t*)p + i);
+    const GB_GLOBAL u4_any2* q = (const GB_GLOBAL u4_any2*)value_at<ET>(p, i);
     u4 v;
     if constexpr (NT) v = __builtin_nontemporal_load(q);
     else v = *q;
@@ -109,7 +119,7 @@ __device__ __forceinline__ Raw<ET, V> load_full(const void* p, size_t i) {
     for (int j = 0; j < 4; j++) r.w[j] = v[j];
   } else {
     static_assert(V == 4, "");
-    const GB_GLOBAL u2_any2* q = (const GB_GLOBAL u2_any2*)((const GB_GLOBAL uint16_t*)p + i);
+    const GB_GLOBAL u2_any2* q = (const GB_GLOBAL u2_any2*)value_at<ET>(p, i);
     u2 v;
     if constexpr (NT) v = __builtin_nontemporal_load(q);
     else v = *q;
@@ -117,8 +127,8 @@ __device__ __forceinline__ Raw<ET, V> load_full(const void* p, size_t i) {
   }
   return r;
 }
-template <int ET, int V, bool NT>
-__device__ __forceinline__ Raw<ET, V> load_raw(const void* p, size_t i, uint32_t left) {
+template <int ET, int V, bool NT, class I>
+__device__ __forceinline__ Raw<ET, V> load_raw(const void* p, I i, uint32_t left) {
   if (left >= V) return load_full<ET, V, NT>(p, i);
   Raw<ET, V> r;
 #pragma unroll
@@ -147,8 +157,8 @@ __device__ __forceinline__ float raw_value(const Raw<ET, V>& r, int e) {
   else return (float)__builtin_bit_cast(h2, r.w[e / 2])[e & 1];
 }
 
-template <int ET, int V, bool NT>
-__device__ __forceinline__ void store_vals(void* p, size_t i, uint32_t left, const float (&v)[V]) {
+template <int ET, int V, bool NT, class I>
+__device__ __forceinline__ void store_vals(void* p, I i, uint32_t left, const float (&v)[V]) {
   if (left >= V) {
     if constexpr (Type<ET>::kSize == 4) {
       static_assert(V % 4 == 0, "");
@@ -156,19 +166,19 @@ __device__ __forceinline__ void store_vals(void* p, size_t i, uint32_t left, con
       for (int j = 0; j < V; j += 4) {
         const u4 w = {__float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
                       __float_as_uint(v[j + 3])};
-        GB_GLOBAL u4_any4* q = (GB_GLOBAL u4_any4*)((GB_GLOBAL uint32_t*)p + i + j);
+        GB_GLOBAL u4_any4* q = (GB_GLOBAL u4_any4*)value_at<ET>(p, (I)(i + j));
         if constexpr (NT) __builtin_nontemporal_store(w, q);
         else *q = w;
       }
     } else if constexpr (V == 8) {
       const u4 w = {half_pair<ET>(v[0], v[1]), half_pair<ET>(v[2], v[3]), half_pair<ET>(v[4], v[5]),
                     half_pair<ET>(v[6], v[7])};
-      GB_GLOBAL u4_any2* q = (GB_GLOBAL u4_any2*)((GB_GLOBAL uint16_t*)p + i);
+      GB_GLOBAL u4_any2* q = (GB_GLOBAL u4_any2*)value_at<ET>(p, i);
       if constexpr (NT) __builtin_nontemporal_store(w, q);
       else *q = w;
     } else {
       const u2 w = {half_pair<ET>(v[0], v[1]), half_pair<ET>(v[2], v[3])};
-      GB_GLOBAL u2_any2* q = (GB_GLOBAL u2_any2*)((GB_GLOBAL uint16_t*)p + i);
+      GB_GLOBAL u2_any2* q = (GB_GLOBAL u2_any2*)value_at<ET>(p, i);
       if constexpr (NT) __builtin_nontemporal_store(w, q);
       else *q = w;
     }
