@@ -40,13 +40,20 @@ struct Team {
   __device__ __forceinline__ bool mine(int k, int e) const {
     return SHORT ? lane == 0 && e < (int)cols : e >= (int)skip[k];
   }
-  __device__ __forceinline__ Raw<ET, V> load(const void* row, int k) const {
-    if constexpr (SHORT) return load_raw<ET, V, true>(row, 0u, lane == 0 ? cols : 0u);
-    else return load_full<ET, V, true>(row, at[k]);
+  // The lane's offset, made anew for each access: hoisted out of a loop, its
+  // widening would take two registers and an addition of 64 bits an access,
+  // where the instruction adds 32 bits to a scalar by itself.
+  __device__ __forceinline__ uint32_t offset(int k) {
+    asm volatile("" : "+v"(at[k]));
+    return at[k];
   }
-  __device__ __forceinline__ void store(void* row, int k, const float (&v)[V]) const {
+  __device__ __forceinline__ Raw<ET, V> load(const void* row, int k) {
+    if constexpr (SHORT) return load_raw<ET, V, true>(row, 0u, lane == 0 ? cols : 0u);
+    else return load_full<ET, V, true>(row, offset(k));
+  }
+  __device__ __forceinline__ void store(void* row, int k, const float (&v)[V]) {
     if constexpr (SHORT) store_vals<ET, V, true>(row, 0u, lane == 0 ? cols : 0u, v);
-    else if (!ragged(k) || skip[k] < V) store_vals<ET, V, true>(row, at[k], V, v);
+    else if (!ragged(k) || skip[k] < V) store_vals<ET, V, true>(row, offset(k), V, v);
   }
   template <int PT>
   __device__ __forceinline__ void param_of(float (&to)[V], const void* p, int k) const {
@@ -115,7 +122,7 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
   using T = Team<ET, L, W, K, SHORT>;
   constexpr int V = T::V, kTeams = THREADS / T::kLanes;
   __shared__ float part[W > 1 ? 2 : 1][W > 1 ? kTeams * W : 1];
-  const T t(a.cols);
+  T t(a.cols);
   const uint32_t team = team_number<L, T::kLanes>();
   float* const sum_part = &part[0][W > 1 ? team * W : 0];
   float* const var_part = &part[W > 1 ? 1 : 0][W > 1 ? team * W : 0];
@@ -212,58 +219,73 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
   constexpr int V = T::V, kTeams = THREADS / T::kLanes;
   // h and g stay in registers between the two passes over a row, or are
   // worked out again from the row's values
-  constexpr bool kKeep = K * V <= 16;
-  // the next row is read ahead while the registers hold it
-  constexpr bool kAhead = K <= 4;
+  constexpr bool kKeep = K * V <= 8;
+  // rows read ahead, as many as the registers hold
+  constexpr int D = K == 1 ? 2 : K == 2 ? 1 : 0;
+  // a lane's weights lie in its registers, or in LDS
+  constexpr bool kWeightsInLds = K * V >= 16;
+  __shared__ f4 lds_w[kWeightsInLds ? K * V / 4 : 1][kWeightsInLds ? THREADS : 1];
   __shared__ float part[2][2][W > 1 ? kTeams * W : 1];
-  const T t(a.cols);
+  T t(a.cols);
   const uint32_t team = team_number<L, T::kLanes>();
   const float inv_n = 1.0f / (float)a.cols;
 
-  Raw<ET, V> x[K], dy[K];
-  float mean, rstd;
-  auto load_row = [&](size_t r) {
+  struct Row {
+    Raw<ET, V> x[K], dy[K];
+    float mean, rstd;
+  };
+  auto load_row = [&](Row& row, size_t r) {
     r = r < a.rows ? r : a.rows - 1;
     const void *const x_row = row_at<ET, L>(a.x, r), *const dy_row = row_at<ET, L>(a.dy, r);
 #pragma unroll
     for (int k = 0; k < K; k++) {
-      x[k] = t.load(x_row, k);
-      dy[k] = t.load(dy_row, k);
+      row.x[k] = t.load(x_row, k);
+      row.dy[k] = t.load(dy_row, k);
     }
-    mean = a.mean[r];
-    rstd = a.rstd[r];
+    row.mean = a.mean[r];
+    row.rstd = a.rstd[r];
   };
+  Row ahead[D > 0 ? D : 1];
   const size_t step = (size_t)gridDim.x * kTeams, first = (size_t)blockIdx.x * kTeams;
-  load_row(first + team);
+#pragma unroll
+  for (int j = 0; j < D; j++) load_row(ahead[j], first + j * step + team);
   float w[K][V], dw[K][V], db[K][V];
   t.param(w, a.w, a.param_dtype, 1.0f);
 #pragma unroll
   for (int k = 0; k < K; k++) {
 #pragma unroll
-    for (int e = 0; e < V; e++) dw[k][e] = db[k][e] = 0.0f;
+    for (int e = 0; e < V; e++) {
+      if constexpr (kWeightsInLds) lds_w[(k * V + e) / 4][threadIdx.x][e % 4] = w[k][e];  // read by this lane alone
+      dw[k][e] = db[k][e] = 0.0f;
+    }
   }
   int parity = 0;
-  for (size_t base = first; base < a.rows; base += step, parity ^= 1) {
+  auto round = [&](Row& row, size_t base) {
     const size_t r = base + team;
-    if (!kAhead && base != first) load_row(r);
+    if (D == 0) load_row(row, r);
+    parity ^= 1;
     if (base + kTeams > a.rows && r >= a.rows) {  // a team without a row adds nothing
 #pragma unroll
-      for (int k = 0; k < K; k++) x[k] = dy[k] = zero_raw<ET, V>();
-      mean = rstd = 0.0f;
+      for (int k = 0; k < K; k++) row.x[k] = row.dy[k] = zero_raw<ET, V>();
+      row.mean = row.rstd = 0.0f;
     }
     float h[kKeep ? K : 1][V], g[kKeep ? K : 1][V], c1 = 0.0f, c2 = 0.0f;
-    const float m = mean, s = rstd;
-    Raw<ET, V> x_now[K], dy_now[K];
+    const float m = row.mean, s = row.rstd;
+    Row now;
 #pragma unroll
     for (int k = 0; k < K; k++) {
-      x_now[k] = x[k];
-      dy_now[k] = dy[k];
+      now.x[k] = row.x[k];
+      now.dy[k] = row.dy[k];
     }
     auto terms = [&](int k, float (&hk)[V], float (&gk)[V]) {
 #pragma unroll
-      for (int e = 0; e < V; e++) {
-        hk[e] = (raw_value<ET, V>(x_now[k], e) - m) * s;
-        gk[e] = raw_value<ET, V>(dy_now[k], e) * w[k][e];
+      for (int j = 0; j < V; j += 4) {
+        const f4 wj = kWeightsInLds ? lds_w[(k * V + j) / 4][threadIdx.x] : f4{w[k][j], w[k][j + 1], w[k][j + 2], w[k][j + 3]};
+#pragma unroll
+        for (int e = j; e < j + 4; e++) {
+          hk[e] = (raw_value<ET, V>(now.x[k], e) - m) * s;
+          gk[e] = raw_value<ET, V>(now.dy[k], e) * wj[e - j];
+        }
       }
     };
 #pragma unroll
@@ -274,7 +296,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
       terms(k, hk, gk);
 #pragma unroll
       for (int e = 0; e < V; e++) {
-        const float d = raw_value<ET, V>(dy_now[k], e);
+        const float d = raw_value<ET, V>(now.dy[k], e);
         dw[k][e] = fmaf(d, hk[e], dw[k][e]);
         db[k][e] += d;
       }
@@ -292,8 +314,8 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
         }
       }
     }
-    if (kAhead && base + step < a.rows) load_row(r + step);
-    if (a.dx.p == nullptr) continue;
+    if (D > 0 && base + D * step < a.rows) load_row(row, r + D * step);
+    if (a.dx.p == nullptr) return;
     c1 = lanes_sum<L>(c1);
     c2 = lanes_sum<L>(c2);
     if constexpr (W > 1) {
@@ -318,11 +340,11 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
       for (int k = 0; k < K; k++) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) asm volatile("" : "+v"(x_now[k].w[j]), "+v"(dy_now[k].w[j]));
+        for (int j = 0; j < 4; j++) asm volatile("" : "+v"(now.x[k].w[j]), "+v"(now.dy[k].w[j]));
       }
     }
     if (r < a.rows) {
-      void* const row = row_at<ET, L>(a.dx, r);
+      void* const to = row_at<ET, L>(a.dx, r);
       // With both sums and rstd finite so are all g and h (an infinite one
       // would show in a sum), and fused products and sums of finite numbers
       // may overflow but have a sign: no value is NaN.
@@ -342,8 +364,14 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
           for (int e = 0; e < V; e++) dx[e] = canon(dx[e]);
         }
-        t.store(row, k, dx);
+        t.store(to, k, dx);
       }
+    }
+  };
+  for (size_t base = first; base < a.rows; base += (D > 0 ? D : 1) * step) {
+#pragma unroll
+    for (int j = 0; j < (D > 0 ? D : 1); j++) {
+      if (base + j * step < a.rows) round(ahead[j], base + j * step);
     }
   }
   if (a.dw == nullptr && a.db == nullptr) return;
@@ -402,27 +430,32 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
 }
 
 // dw and db from the workgroups' partial sums: 4 columns a lane, 16 lanes side
-// by side, and 16 (kSlices) of those take every 16th partial each; their sums
-// are joined in order.  blockIdx.y: dw or db.
-constexpr int kJoinLanes = 16, kSlices = 16;
+// by side, and 64 (kSlices) of those take every 64th partial each; their sums
+// are joined in order, by eights.  blockIdx.y: dw or db.
+constexpr int kJoinLanes = 16, kSlices = 64;
 __global__ __launch_bounds__(kJoinLanes* kSlices) void norm_join_kernel(NormGradArgs a, uint32_t groups) {
   __shared__ f4 slice[kSlices][kJoinLanes];
   void* const out = blockIdx.y == 0 ? a.dw : a.db;
   if (out == nullptr) return;
   const uint32_t l = threadIdx.x % kJoinLanes, s = threadIdx.x / kJoinLanes;
   const uint32_t col = (blockIdx.x * kJoinLanes + l) * 4;
-  const size_t stride = a.partial_stride;
-  const float* const p = a.partials + blockIdx.y * stride + col;
+  const float* const p = a.partials + blockIdx.y * a.partial_stride + col;
   f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
   if (col < a.cols) {
-#pragma unroll 8
-    for (uint32_t g = s; g < groups; g += kSlices) v += *(const f4*)(p + (size_t)g * 2 * stride);
+#pragma unroll 4
+    for (uint32_t g = s; g < groups; g += kSlices) v += *(const f4*)(p + (size_t)g * 2 * a.partial_stride);
   }
   slice[s][l] = v;
   __syncthreads();
+  if (s % 8 == 0) {
+#pragma unroll
+    for (int i = 1; i < 8; i++) v += slice[s + i][l];
+    slice[s][l] = v;
+  }
+  __syncthreads();
   if (s != 0 || col >= a.cols) return;
 #pragma unroll
-  for (int i = 1; i < kSlices; i++) v += slice[i][l];
+  for (int i = 8; i < kSlices; i += 8) v += slice[i][l];
 #pragma unroll
   for (int e = 0; e < 4; e++) {
     if (col + e >= a.cols) break;
@@ -438,45 +471,43 @@ __global__ __launch_bounds__(kJoinLanes* kSlices) void norm_join_kernel(NormGrad
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-template <int ET, int L, int W, int K, bool SHORT = false>
+template <int ET, int L, int W, int K, int THREADS, bool SHORT = false>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
-  constexpr int kThreads = W > 4 ? W * kWave : 256;
-  constexpr size_t kTeams = kThreads / (L * W);
+  constexpr size_t kTeams = THREADS / (L * W), kMost = 512 * 512 / THREADS * (W > 2 ? 1 : 2);
   size_t grid = (a.rows + kTeams - 1) / kTeams;
-  if (grid > 2048) grid = 2048;
-  norm_kernel<ET, L, W, K, kThreads, SHORT><<<dim3((unsigned)grid), dim3(kThreads), 0, stream>>>(a);
+  if (grid > kMost) grid = kMost;
+  norm_kernel<ET, L, W, K, THREADS, SHORT><<<dim3((unsigned)grid), dim3(THREADS), 0, stream>>>(a);
   return hipGetLastError();
 }
 template <int ET>
 hipError_t pick_norm(const NormArgs& a, hipStream_t stream) {
   const uint32_t v = (a.cols + Type<ET>::kVec - 1) / Type<ET>::kVec;
-  if (a.cols < Type<ET>::kVec) return run_norm<ET, 8, 1, 1, true>(a, stream);
-  if (v <= 8) return run_norm<ET, 8, 1, 1>(a, stream);
-  if (v <= 16) return run_norm<ET, 16, 1, 1>(a, stream);
-  if (v <= 32) return run_norm<ET, 32, 1, 1>(a, stream);
-  if (v <= 64) return run_norm<ET, 64, 1, 1>(a, stream);
-  if (v <= 128) return run_norm<ET, 64, 1, 2>(a, stream);
-  if (v <= 256) return run_norm<ET, 64, 2, 2>(a, stream);
-  if (v <= 512) return run_norm<ET, 64, 4, 2>(a, stream);
-  if (v <= 1024) return run_norm<ET, 64, 4, 4>(a, stream);
-  if (v <= 2048) return run_norm<ET, 64, 8, 4>(a, stream);
+  if (a.cols < Type<ET>::kVec) return run_norm<ET, 8, 1, 1, 256, true>(a, stream);
+  if (v <= 8) return run_norm<ET, 8, 1, 1, 256>(a, stream);
+  if (v <= 16) return run_norm<ET, 16, 1, 1, 256>(a, stream);
+  if (v <= 32) return run_norm<ET, 32, 1, 1, 256>(a, stream);
+  if (v <= 64) return run_norm<ET, 64, 1, 1, 256>(a, stream);
+  if (v <= 128) return run_norm<ET, 64, 2, 1, 256>(a, stream);
+  if (v <= 256) return run_norm<ET, 64, 4, 1, 512>(a, stream);
+  if (v <= 512) return run_norm<ET, 64, 8, 1, 512>(a, stream);
+  if (v <= 1024) return run_norm<ET, 64, 8, 2, 512>(a, stream);
+  if (v <= 2048) return run_norm<ET, 64, 16, 2, 1024>(a, stream);
   if constexpr (ET == GB_DTYPE_F32) {
-    if (v > 4096) return run_norm<ET, 64, 16, 8>(a, stream);
+    if (v > 4096) return run_norm<ET, 64, 16, 8, 1024>(a, stream);
   }
-  return run_norm<ET, 64, 16, 4>(a, stream);
+  return run_norm<ET, 64, 16, 4, 1024>(a, stream);
 }
 
-template <int ET, int L, int W, int K, bool SHORT = false>
+template <int ET, int L, int W, int K, int THREADS, bool SHORT = false>
 struct NormGrad {
-  static constexpr int kThreads = W > 4 ? W * kWave : 256;
-  static constexpr size_t kTeams = kThreads / (L * W);
+  static constexpr size_t kTeams = THREADS / (L * W), kMost = 256 * 1024 / THREADS;
   static uint32_t groups(size_t rows, size_t) {
     const size_t g = (rows + kTeams - 1) / kTeams;
-    return (uint32_t)(g < 512 ? g : 512);
+    return (uint32_t)(g < kMost ? g : kMost);
   }
   static hipError_t run(const NormGradArgs& a, hipStream_t stream) {
     const uint32_t g = groups(a.rows, a.cols);
-    if (g > 0) norm_grad_kernel<ET, L, W, K, kThreads, SHORT><<<dim3(g), dim3(kThreads), 0, stream>>>(a);
+    if (g > 0) norm_grad_kernel<ET, L, W, K, THREADS, SHORT><<<dim3(g), dim3(THREADS), 0, stream>>>(a);
     return hipGetLastError();
   }
 };
@@ -484,20 +515,20 @@ struct NormGrad {
 template <int ET, class F>
 auto with_norm_grad(size_t cols, F&& f) {
   const size_t v = (cols + Type<ET>::kVec - 1) / Type<ET>::kVec;
-  if (cols < Type<ET>::kVec) return f(NormGrad<ET, 8, 1, 1, true>());
-  if (v <= 8) return f(NormGrad<ET, 8, 1, 1>());
-  if (v <= 16) return f(NormGrad<ET, 16, 1, 1>());
-  if (v <= 32) return f(NormGrad<ET, 32, 1, 1>());
-  if (v <= 64) return f(NormGrad<ET, 64, 1, 1>());
-  if (v <= 128) return f(NormGrad<ET, 64, 1, 2>());
-  if (v <= 256) return f(NormGrad<ET, 64, 2, 2>());
-  if (v <= 512) return f(NormGrad<ET, 64, 4, 2>());
-  if (v <= 1024) return f(NormGrad<ET, 64, 4, 4>());
-  if (v <= 2048) return f(NormGrad<ET, 64, 8, 4>());
+  if (cols < Type<ET>::kVec) return f(NormGrad<ET, 8, 1, 1, 256, true>());
+  if (v <= 8) return f(NormGrad<ET, 8, 1, 1, 1024>());
+  if (v <= 16) return f(NormGrad<ET, 16, 1, 1, 1024>());
+  if (v <= 32) return f(NormGrad<ET, 32, 1, 1, 1024>());
+  if (v <= 64) return f(NormGrad<ET, 64, 1, 1, 1024>());
+  if (v <= 128) return f(NormGrad<ET, 64, 2, 1, 1024>());
+  if (v <= 256) return f(NormGrad<ET, 64, 4, 1, 1024>());
+  if (v <= 512) return f(NormGrad<ET, 64, 8, 1, 1024>());
+  if (v <= 1024) return f(NormGrad<ET, 64, 16, 1, 1024>());
+  if (v <= 2048) return f(NormGrad<ET, 64, 16, 2, 1024>());
   if constexpr (ET == GB_DTYPE_F32) {
-    if (v > 4096) return f(NormGrad<ET, 64, 8, 16>());
+    if (v > 4096) return f(NormGrad<ET, 64, 16, 8, 1024>());
   }
-  return f(NormGrad<ET, 64, 8, 8>());
+  return f(NormGrad<ET, 64, 16, 4, 1024>());
 }
 template <class F>
 auto with_norm_grad(int dtype, size_t cols, F&& f) {
