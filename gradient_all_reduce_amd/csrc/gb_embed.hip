@@ -83,14 +83,15 @@ __device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
-// Ranks I digits a lane within the wavefront, item i of the lanes before item
+// Ranks `items` (I at most) digits a lane within the wavefront, item i of the lanes before item
 // i + 1: rank[i] counts the equal digits before it, and counts[digit] ends as
 // their number.  counts: zeroed, this wavefront's own.
 template <int I>
-__device__ __forceinline__ void rank_wave(const uint32_t (&digit)[I], const bool (&valid)[I], uint32_t bits,
-                                          volatile uint16_t* counts, uint32_t (&rank)[I]) {
+__device__ __forceinline__ void rank_wave(const uint32_t (&digit)[I], const bool (&valid)[I], uint32_t items,
+                                          uint32_t bits, volatile uint16_t* counts, uint32_t (&rank)[I]) {
 #pragma unroll
   for (int i = 0; i < I; i++) {
+    if (i >= (int)items) break;
     const uint64_t same = same_digit(digit[i], valid[i], bits);
     const uint32_t below = lanes_below(same);
     if (valid[i]) {
@@ -124,10 +125,18 @@ __device__ __forceinline__ uint32_t scan_lanes(uint32_t v, uint32_t* waves, uint
   return before + s - v;
 }
 
+// Clears the flags of the rows: part of parts.  (An array of whole 256 bytes.)
+__device__ __forceinline__ void clear_named(const LookGradArgs& a, uint8_t* named, uint32_t part, uint32_t parts) {
+  const size_t words = (a.vocab + 15) / 16;
+  for (size_t i = (size_t)part * kSortThreads + threadIdx.x; i < words; i += (size_t)parts * kSortThreads) {
+    ((u4*)named)[i] = u4{0u, 0u, 0u, 0u};
+  }
+}
+
 // One workgroup sorts up to kSortSmall tokens, in LDS between the passes.
 constexpr int kSmallItems = kSortSmall / kSortThreads;
 __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(LookGradArgs a, Digits d, uint32_t* count,
-                                                                  uint32_t* keys, uint32_t* tokens) {
+                                                                  uint32_t* keys, uint32_t* tokens, uint8_t* named) {
   __shared__ uint32_t row_of_slot[kSortSmall], token_of_slot[kSortSmall];
   __shared__ uint16_t counts[kSortWaves][kBins];
   __shared__ uint32_t start[kBins], waves[kSortWaves];
@@ -144,8 +153,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(LookGradArgs a
     valid[i] = i < (int)rounds && token[i] < a.tokens && token_row(a, token[i], key[i]);
   }
   uint32_t n = 0;
+  if (named != nullptr) clear_named(a, named, 0, 1);
   for (uint32_t pass = 0; pass < d.passes; pass++) {
-    for (uint32_t i = threadIdx.x; i < kSortWaves * kBins / 2; i += kSortThreads) ((uint32_t*)counts)[i] = 0u;
+    for (uint32_t w = 0; w < kSortWaves; w++) counts[w][threadIdx.x] = 0;
     if (pass > 0) {
 #pragma unroll
       for (int i = 0; i < kSmallItems; i++) {
@@ -157,13 +167,15 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(LookGradArgs a
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSmallItems; i++) digit[i] = (key[i] >> (pass * d.bits)) & ((1u << d.bits) - 1u);
-    rank_wave<kSmallItems>(digit, valid, d.bits, counts[wave], rank);
+    rank_wave<kSmallItems>(digit, valid, rounds, d.bits, counts[wave], rank);
     __syncthreads();
-    uint32_t sum = 0;
+    uint32_t sum = 0, c[kSortWaves];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; w++) c[w] = counts[w][threadIdx.x];
+#pragma unroll
     for (int w = 0; w < kSortWaves; w++) {
-      const uint32_t c = counts[w][threadIdx.x];
       counts[w][threadIdx.x] = (uint16_t)sum;
-      sum += c;
+      sum += c[w];
     }
     const uint32_t before = scan_lanes(sum, waves, &n);
     start[threadIdx.x] = before;
@@ -176,6 +188,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(LookGradArgs a
       if (last) {
         keys[to] = key[i];
         tokens[to] = token[i];
+        if (named != nullptr) named[key[i]] = 1;
       } else {
         row_of_slot[to] = key[i];
         token_of_slot[to] = token[i];
@@ -183,7 +196,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(LookGradArgs a
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) *count = n;
+  if (threadIdx.x == 0) {
+    count[0] = n;
+    count[1] = 0u;  // long runs, which the sums count
+  }
 }
 
 // A digit pass over more tokens: workgroup b of gridDim.x takes a run of whole
@@ -193,6 +209,7 @@ struct DigitPass {
   const uint32_t* tokens;
   const uint32_t* count;   // tokens in them
   uint32_t* hist;          // [workgroups][bins]
+  uint8_t* named;          // flags of the rows that the first pass sets, or NULL
   uint32_t shift, bits;
 };
 __device__ __forceinline__ size_t block_tokens(size_t tokens) {
@@ -214,6 +231,7 @@ __device__ __forceinline__ bool pass_item(const LookGradArgs& a, const DigitPass
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(LookGradArgs a, DigitPass p) {
   __shared__ uint32_t bins[kBins];
   bins[threadIdx.x] = 0u;
+  if (p.keys == nullptr && p.named != nullptr) clear_named(a, p.named, blockIdx.x, gridDim.x);
   __syncthreads();
   const size_t n = p.keys == nullptr ? a.tokens : *p.count, each = block_tokens(a.tokens);
   const size_t from = blockIdx.x * each, to = from + each < n ? from + each : n;
@@ -222,49 +240,73 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(LookGradArgs a
     if (pass_item(a, p, at, n, key, token)) atomicAdd(&bins[(key >> p.shift) & ((1u << p.bits) - 1u)], 1u);
   }
   __syncthreads();
-  p.hist[(size_t)blockIdx.x * kBins + threadIdx.x] = bins[threadIdx.x];
+  if (threadIdx.x >> p.bits == 0) p.hist[((size_t)blockIdx.x << p.bits) + threadIdx.x] = bins[threadIdx.x];
 }
 
 constexpr int kTileItems = kSortTile / kSortThreads;
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(LookGradArgs a, DigitPass p, uint32_t* keys,
                                                                     uint32_t* tokens, uint32_t* count) {
   __shared__ uint16_t counts[kSortWaves][kBins];
-  __shared__ uint32_t start[kBins], waves[kSortWaves];
+  __shared__ uint32_t start[kBins], waves[kSortWaves], sums[2][kSortThreads];
   const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  // where this workgroup's tokens of each bin begin: after all smaller bins,
-  // and after the earlier workgroups' tokens of the same bin
-  uint32_t mine = 0, sum = 0;
-#pragma unroll 8
-  for (uint32_t b = 0; b < gridDim.x; b++) {
-    const uint32_t c = p.hist[(size_t)b * kBins + threadIdx.x];
-    if (b < blockIdx.x) mine += c;
-    sum += c;
-  }
-  uint32_t total;
-  uint32_t begin = scan_lanes(sum, waves, &total) + mine;
+  const uint32_t bin = threadIdx.x & ((1u << p.bits) - 1u);
+  const bool owner = threadIdx.x >> p.bits == 0;  // of the bin
   const size_t n = p.keys == nullptr ? a.tokens : *p.count, each = block_tokens(a.tokens);
   const size_t from = blockIdx.x * each, to = from + each < n ? from + each : n;
-  for (size_t tile = from; tile < to; tile += kSortTile) {
-    for (uint32_t i = threadIdx.x; i < kSortWaves * kBins / 2; i += kSortThreads) ((uint32_t*)counts)[i] = 0u;
-    start[threadIdx.x] = begin;
-    uint32_t key[kTileItems], token[kTileItems], digit[kTileItems], rank[kTileItems];
-    bool valid[kTileItems];
+  uint32_t key[kTileItems], token[kTileItems], digit[kTileItems], rank[kTileItems];
+  bool valid[kTileItems];
+  auto load_tile = [&](size_t tile) {
 #pragma unroll
     for (int i = 0; i < kTileItems; i++) {
       key[i] = 0;
-      valid[i] = pass_item(a, p, tile + (wave * kTileItems + i) * kWave + lane, n, key[i], token[i]);
+      valid[i] = pass_item(a, p, tile + (wave * kTileItems + i) * kWave + lane, to, key[i], token[i]);
       digit[i] = (key[i] >> p.shift) & ((1u << p.bits) - 1u);
     }
-    __syncthreads();
-    rank_wave<kTileItems>(digit, valid, p.bits, counts[wave], rank);
-    __syncthreads();
-    uint32_t in_tile = 0;
-    for (int w = 0; w < kSortWaves; w++) {
-      const uint32_t c = counts[w][threadIdx.x];
-      counts[w][threadIdx.x] = (uint16_t)in_tile;
-      in_tile += c;
+  };
+  load_tile(from);
+  // where this workgroup's tokens of each bin begin: after all smaller bins,
+  // and after the earlier workgroups' tokens of the same bin.  With fewer bins
+  // than lanes several lanes share the workgroups of a bin.
+  uint32_t mine = 0, sum = 0;
+#pragma unroll 16
+  for (uint32_t b = threadIdx.x >> p.bits; b < gridDim.x; b += kSortThreads >> p.bits) {
+    const uint32_t c = p.hist[((size_t)b << p.bits) + bin];
+    if (b < blockIdx.x) mine += c;
+    sum += c;
+  }
+  sums[0][threadIdx.x] = sum;
+  sums[1][threadIdx.x] = mine;
+  __syncthreads();
+  if (owner) {
+    for (uint32_t i = threadIdx.x + (1u << p.bits); i < kSortThreads; i += 1u << p.bits) {
+      sum += sums[0][i];
+      mine += sums[1][i];
     }
-    begin += in_tile;
+  } else {
+    sum = mine = 0;
+  }
+  uint32_t total;
+  uint32_t begin = scan_lanes(sum, waves, &total) + mine;
+  for (size_t tile = from; tile < to; tile += kSortTile) {
+    if (tile != from) load_tile(tile);
+    if (owner) {
+      for (uint32_t w = 0; w < kSortWaves; w++) counts[w][bin] = 0;
+      start[bin] = begin;
+    }
+    __syncthreads();
+    rank_wave<kTileItems>(digit, valid, kTileItems, p.bits, counts[wave], rank);
+    __syncthreads();
+    if (owner) {
+      uint32_t in_tile = 0, c[kSortWaves];
+#pragma unroll
+      for (int w = 0; w < kSortWaves; w++) c[w] = counts[w][bin];
+#pragma unroll
+      for (int w = 0; w < kSortWaves; w++) {
+        counts[w][bin] = (uint16_t)in_tile;
+        in_tile += c[w];
+      }
+      begin += in_tile;
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kTileItems; i++) {
@@ -272,87 +314,111 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(LookGradArgs
       const uint32_t at = start[digit[i]] + counts[wave][digit[i]] + rank[i];
       keys[at] = key[i];
       tokens[at] = token[i];
+      if (p.keys == nullptr && p.named != nullptr) p.named[key[i]] = 1;
     }
     __syncthreads();
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *count = total;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    count[0] = total;
+    count[1] = 0u;  // long runs, which the sums count
+  }
 }
 
 // ---------------------------------------------------------------------------
 // The sums.  A run is the sorted tokens of one row; its folds begin at every
 // kFold-th token from its start.  A wavefront takes the folds that begin in a
-// window of kFold sorted tokens, for a slab of columns: the sum of a run of
+// window of kWindow sorted tokens, for a slab of columns: the sum of a run of
 // one fold goes to the table, any other fold's to the partials, where the join
-// finds it.  Of two folds of longer runs that begin in one window, one ends a
-// run (it is not that run's first) and one begins a run, since the folds of a
-// run lie exactly a window apart and a run of one fold leaves no partial.
+// finds it.  Two folds of longer runs that begin among the same kFold tokens:
+// one ends a run (it is not that run's first) and one begins a run, since the
+// folds of a run lie kFold apart and a run of one fold leaves no partial.
 // ---------------------------------------------------------------------------
+constexpr uint32_t kWindow = 16;
+static_assert(kFold % kWindow == 0 && kFold == kWave, "a fold is a lane each");
+
 struct Sorted {
-  const uint32_t* count;  // NULL: no tokens
+  uint32_t* count;       // tokens that name a row; NULL: no tokens
+  uint32_t* long_count;  // runs of more than one fold, and where they begin
+  uint32_t* long_runs;
   const uint32_t* keys;
   const uint32_t* tokens;
   float* partials;
-  size_t stride;  // of the partials
+  size_t stride;   // of the partials
+  uint8_t* named;  // whether a token names a row; NULL where no row needs zeros, or none has a token
 };
 __device__ __forceinline__ size_t partial_slot(uint32_t fold_start, bool begins_run) {
   return 2 * (size_t)(fold_start / kFold) + (begins_run ? 1 : 0);
 }
 
-// First position in [0, n) whose key is at least key (n if none).
+// First position in [0, n) whose key is at least key (n if none): all lanes
+// look at once, so a step divides the range by 65.  key is the same in all.
 __device__ __forceinline__ uint32_t lower_bound(const uint32_t* keys, uint32_t n, uint32_t key) {
+  const uint32_t lane = threadIdx.x % kWave;
   uint32_t lo = 0, hi = n;
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (keys[mid] < key) lo = mid + 1;
-    else hi = mid;
+  while (hi - lo > 0) {
+    // lanes look at 64 places that cut [lo, hi) into 65 pieces, the first at lo + each
+    const uint32_t each = (hi - lo) / (kWave + 1);
+    const uint32_t at = lo + each + lane * (each + 1);
+    const uint32_t less = __popcll(__ballot(at < hi && keys[at] < key));
+    const uint32_t next = lo + each + less * (each + 1);  // the first place not below key
+    lo = less == 0 ? lo : next - (each + 1) + 1;
+    hi = next < hi ? next : hi;
   }
   return lo;
 }
 
-// A row of the table from its sum.
-template <int GT, int V>
+// A wavefront's slab is a vector in each lane, the shorter one of the two
+// types, so that every access of an instruction is one contiguous run (two
+// 16-byte halves of a lane's 8 float32 values would each touch every line,
+// and the non-temporal hint lets a line go after the first).
+template <int ET, int GT>
+struct Slab {
+  static constexpr int V = Type<ET>::kVec < Type<GT>::kVec ? Type<ET>::kVec : Type<GT>::kVec;
+  static constexpr uint32_t kCols = kWave * V;
+};
+
+// A row of the table from its sum and, with ADD, what it held.
+template <int GT, int V, bool ADD>
 __device__ __forceinline__ void store_row(const LookGradArgs& a, uint32_t row, uint32_t col, uint32_t left,
-                                          const float (&sum)[V]) {
-  const size_t at = (size_t)row * a.dtable.stride + col;
+                                          const float (&sum)[V], const Raw<GT, V>& old) {
+  char* const to = (char*)a.dtable.p + (size_t)row * a.dtable.stride * Type<GT>::kSize;
   float v[V];
-  constexpr int kPart = Type<GT>::kVec < V ? Type<GT>::kVec : V;
-  Raw<GT, kPart> old[V / kPart];
-  if (a.accumulate) {
-#pragma unroll
-    for (int j = 0; j < V / kPart; j++) {
-      old[j] = load_raw<GT, kPart, false>(a.dtable.p, at + j * kPart,
-                                          left > (uint32_t)(j * kPart) ? left - j * kPart : 0u);
-    }
-  }
 #pragma unroll
   for (int e = 0; e < V; e++) {
     v[e] = sum[e] * a.scale;
-    if (a.accumulate) v[e] = raw_value<GT, kPart>(old[e / kPart], e % kPart) + v[e];
+    if constexpr (ADD) v[e] = raw_value<GT, V>(old, e) + v[e];
     v[e] = canon(v[e]);
   }
-  store_vals<GT, V, true>(a.dtable.p, at, left, v);
+  store_vals<GT, V, true>(to, col, left, v);
 }
 
 constexpr int kSumWaves = 4;
-template <int ET, int GT>
+constexpr uint32_t kXcds = 8;
+template <int ET, int GT, bool ADD, bool FULL>
 __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& s, uint32_t window, uint32_t slab) {
-  constexpr int V = Type<ET>::kVec, U = 4;
-  const uint32_t n = *s.count, p0 = window * kFold, lane = threadIdx.x % kWave;
+  constexpr int V = Slab<ET, GT>::V, U = 8;
+  const uint32_t p0 = window * kWindow, lane = threadIdx.x % kWave;
+  const uint32_t pa = p0 + lane, pb = p0 + kFold + lane, tokens = (uint32_t)a.tokens;
+  // read before their number is known: what lies beyond it is not looked at
+  uint32_t key_a = s.keys[pa < tokens ? pa : 0], key_b = s.keys[pb < tokens ? pb : 0];
+  const uint32_t before = s.keys[pa > 0 && pa < tokens ? pa - 1 : 0];
+  const uint32_t token_a = s.tokens[pa < tokens ? pa : 0], token_b = s.tokens[pb < tokens ? pb : 0];
+  const uint32_t n = *s.count;
   if (p0 >= n) return;
-  const uint32_t col = (slab * kWave + lane) * V, left = left_of(col, (uint32_t)a.dim);
-  const uint32_t pa = p0 + lane, pb = p0 + kFold + lane;
-  const uint32_t key_a = pa < n ? s.keys[pa] : ~0u, key_b = pb < n ? s.keys[pb] : ~0u;
-  const uint32_t token_a = pa < n ? s.tokens[pa] : 0u, token_b = pb < n ? s.tokens[pb] : 0u;
-  const uint32_t before = pa > 0 && pa < n ? s.keys[pa - 1] : ~0u;
-  // where runs begin in the window, and whether one goes on into it
-  uint64_t starts = __ballot(pa < n && (pa == 0 || before != key_a));
+  key_a = pa < n ? key_a : ~0u;
+  key_b = pb < n ? key_b : ~0u;
+  uint32_t col = (slab * kWave + lane) * V;
+  const uint32_t left = FULL ? V : left_of(col, (uint32_t)a.dim);
+  // where runs begin in the lanes' tokens, and whether one goes on into them
+  const uint64_t starts = __ballot(pa < n && (pa == 0 || before != key_a));
   uint64_t heads = starts;
   if (!(starts & 1u)) {
     const uint32_t key = __builtin_amdgcn_readfirstlane(key_a);
-    const uint32_t offset = (lower_bound(s.keys, n, key) - p0) % kFold;  // of its fold in this window
+    const uint32_t offset = (lower_bound(s.keys, p0, key) - p0) % kFold;  // of its next fold from here
     const uint64_t same = __ballot(pa < n && key_a == key);
     if ((same >> offset) & 1u) heads |= (uint64_t)1 << offset;
   }
+  heads &= ((uint64_t)1 << kWindow) - 1;
   if (heads == 0) return;
   // the last fold may end beyond the window
   const uint32_t last = 63 - __clzll(heads);
@@ -362,20 +428,29 @@ __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& 
   const uint32_t end = last + __popcll(tail_a) + __popcll(tail_b);
   // runs of more than one fold
   const uint64_t more = __ballot(pb < n && key_b == key_a);
+  const uint64_t whole = starts & ~more;  // runs of one fold: their sums are the table's
+  if (slab == 0 && lane < kWindow && ((starts & more) >> lane & 1u)) {
+    // the join's work list; its order changes no result
+    s.long_runs[atomicAdd(s.long_count, 1u)] = pa;
+  }
 
   float acc[V];
-  uint32_t at = __ffsll((unsigned long long)heads) - 1;
-  uint32_t head = at;
-  while (at < end) {
-    Raw<ET, V> x[U];
+  Raw<ET, V> x[U];
+  Raw<GT, V> old[ADD ? U : 1], now;
+  uint32_t head = __ffsll((unsigned long long)heads) - 1;
+  for (uint32_t at = head; at < end; at += U) {
+    asm volatile("" : "+v"(col));  // a lane's offset of 32 bits, not widened ahead of the loop
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const uint32_t i = at + u;
-      if (i < end) {
-        const uint32_t t = i < 64 ? __builtin_amdgcn_readlane(token_a, i) : __builtin_amdgcn_readlane(token_b, i - 64);
-        x[u] = load_raw<ET, V, true>(a.dout.p, (size_t)t * a.dout.stride + col, left);
-      } else {
-        x[u] = zero_raw<ET, V>();
+      const uint32_t i = at + u < end ? at + u : end - 1;
+      const uint32_t t = i < 64 ? __builtin_amdgcn_readlane(token_a, i) : __builtin_amdgcn_readlane(token_b, i - 64);
+      x[u] = load_raw<ET, V, true>((const char*)a.dout.p + (size_t)t * a.dout.stride * Type<ET>::kSize, col, left);
+      if constexpr (ADD) {
+        if (i < 64 && ((whole >> i) & 1u)) {
+          const uint32_t row = __builtin_amdgcn_readlane(key_a, i);
+          old[u] = load_raw<GT, V, true>((const char*)a.dtable.p + (size_t)row * a.dtable.stride * Type<GT>::kSize, col,
+                                         left);
+        }
       }
     }
 #pragma unroll
@@ -383,18 +458,20 @@ __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& 
       const uint32_t i = at + u;
       if (i >= end) break;
       const bool begins = i < 64 && ((heads >> i) & 1u);
-      if (begins) head = i;
+      if (begins) {
+        head = i;
+        if constexpr (ADD) now = old[u];
+      }
 #pragma unroll
       for (int e = 0; e < V; e++) {
         const float v = raw_value<ET, V>(x[u], e);
         acc[e] = begins ? v : acc[e] + v;
       }
       if (i + 1 == end || (i + 1 < 64 && ((heads >> (i + 1)) & 1u))) {
-        const bool first = (starts >> head) & 1u;
-        if (first && !((more >> head) & 1u)) {
-          store_row<GT, V>(a, __builtin_amdgcn_readlane(key_a, head), col, left, acc);
+        if ((whole >> head) & 1u) {
+          store_row<GT, V, ADD>(a, __builtin_amdgcn_readlane(key_a, head), col, left, acc, now);
         } else {
-          float* const out = s.partials + partial_slot(p0 + head, first) * s.stride;
+          float* const out = s.partials + partial_slot(p0 + head, (starts >> head) & 1u) * s.stride;
 #pragma unroll
           for (int j = 0; j < V; j += 4) {
             const float v[4] = {acc[j], acc[j + 1], acc[j + 2], acc[j + 3]};
@@ -403,7 +480,6 @@ __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& 
         }
       }
     }
-    at += U;
   }
 }
 
@@ -411,80 +487,83 @@ __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& 
 template <int GT>
 __device__ __forceinline__ void zero_rows(const LookGradArgs& a, const Sorted& s, size_t row, uint32_t rows) {
   const uint32_t lane = threadIdx.x % kWave;
-  const uint32_t n = s.count != nullptr ? *s.count : 0u;
+  if (row >= a.vocab) return;
   const bool mine = lane < rows && row + lane < a.vocab;
-  const uint32_t r = (uint32_t)(row + lane);
-  bool empty = mine;
-  if (mine && n > 0) {
-    const uint32_t at = lower_bound(s.keys, n, r);
-    empty = at == n || s.keys[at] != r;
-  }
-  const uint64_t todo = __ballot(empty);
-  constexpr int V = Type<GT>::kVec;
-  float zero[V];
-#pragma unroll
-  for (int e = 0; e < V; e++) zero[e] = 0.0f;
-  for (uint32_t i = threadIdx.x / kWave; i < rows; i += kSumWaves) {
+  const uint64_t todo = __ballot(mine && (s.named == nullptr || s.named[row + lane] == 0));
+  constexpr uint32_t V = Type<GT>::kVec;
+  const float zero[V] = {};
+  const uint32_t dim = (uint32_t)a.dim;
+  for (uint32_t i = 0; i < rows; i++) {
     if (!((todo >> i) & 1u)) continue;
-    const size_t at = (row + i) * a.dtable.stride;
-    for (size_t c = lane * V; c < a.dim; c += kWave * V) {
-      store_vals<GT, V, true>(a.dtable.p, at + c, left_of((uint32_t)c, (uint32_t)a.dim), zero);
-    }
+    char* const to = (char*)a.dtable.p + (row + i) * a.dtable.stride * Type<GT>::kSize;
+    uint32_t c = threadIdx.x * V;
+    for (; c + V <= dim; c += kSumWaves * kWave * V) store_vals<GT, (int)V, false>(to, c, V, zero);
+    if (c < dim) store_vals<GT, (int)V, false>(to, c, dim - c, zero);
   }
 }
 
 // Workgroups [0, sums) take windows and slabs, the rest rows without a token.
-template <int ET, int GT>
+template <int ET, int GT, bool ADD>
 __global__ __launch_bounds__(kSumWaves* kWave) void embedding_sum_kernel(LookGradArgs a, Sorted s, uint32_t sums,
                                                                         uint32_t slabs, size_t units,
                                                                         uint32_t zero_each) {
-  if (blockIdx.x < sums) {
+  if (ADD || blockIdx.x < sums) {
     const size_t unit = (size_t)blockIdx.x * kSumWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    if (unit < units) sum_window<ET, GT>(a, s, (uint32_t)(unit / slabs), (uint32_t)(unit % slabs));
+    if (unit >= units) return;
+    const uint32_t window = (uint32_t)(unit / slabs), slab = (uint32_t)(unit % slabs);
+    if ((slab + 1) * Slab<ET, GT>::kCols <= a.dim) sum_window<ET, GT, ADD, true>(a, s, window, slab);
+    else sum_window<ET, GT, ADD, false>(a, s, window, slab);
   } else {
-    zero_rows<GT>(a, s, (size_t)(blockIdx.x - sums) * zero_each, zero_each);
+    // workgroups go to the 8 XCDs in turn: each XCD's rows lie together
+    const uint32_t z = blockIdx.x - sums, per_xcd = (gridDim.x - sums) / kXcds;
+    zero_rows<GT>(a, s, ((size_t)(z % kXcds) * per_xcd + z / kXcds) * zero_each, zero_each);
   }
 }
 
-// The sums of runs of several folds: a workgroup takes the run that begins in
-// its window, if it is such a run (two of them begin more than a window
-// apart), for a slab of 256 columns.  Level by level kFold sums are added in
-// order, each wavefront taking every kJoinWaves-th of a level's groups.
+// The sums of runs of several folds: a workgroup takes a run of the work list
+// for a slab of 64 columns at a time.  Level by level kFold sums are added in
+// order, each wavefront taking every kJoinWaves-th of a level's groups, all of
+// a group's loads in flight at once.
 constexpr int kJoinWaves = 4;
 template <int GT>
-__global__ __launch_bounds__(kJoinWaves* kWave) void embedding_join_kernel(LookGradArgs a, Sorted s) {
-  const uint32_t n = *s.count, p0 = blockIdx.x * kFold, lane = threadIdx.x % kWave;
-  if (p0 >= n) return;
-  const uint32_t p = p0 + lane, key = p < n ? s.keys[p] : 0u;
-  const bool head = p + kFold < n && s.keys[p + kFold] == key && (p == 0 || s.keys[p - 1] != key);
-  const uint64_t heads = __ballot(head);
-  if (heads == 0) return;
-  const uint32_t at = __ffsll((unsigned long long)heads) - 1, start = p0 + at;
-  const uint32_t row = __builtin_amdgcn_readlane(key, at);
-  const uint32_t length = (row == ~0u ? n : lower_bound(s.keys, n, row + 1)) - start;
-  const uint32_t col = (blockIdx.y * kWave + lane) * 4, left = left_of(col, (uint32_t)a.dim);
-  const uint32_t wave = threadIdx.x / kWave;
-  auto slot = [&](uint32_t fold) {
-    return s.partials + partial_slot(start + fold * kFold, fold == 0) * s.stride + col;
-  };
-  uint32_t level = 1;  // a level's sums stand in every level-th fold's slot
-  for (uint32_t sums = (length + kFold - 1) / kFold; sums > 1; sums = (sums + kFold - 1) / kFold) {
-    for (uint32_t g = wave; g * kFold < sums; g += kJoinWaves) {
-      const uint32_t from = g * kFold, to = from + kFold < sums ? from + kFold : sums;
-      if (left > 0) {
-        f4 v = *(const f4*)slot(from * level);
-#pragma unroll 8
-        for (uint32_t i = from + 1; i < to; i++) v += *(const f4*)slot(i * level);
-        *(f4*)slot(from * level) = v;
+__global__ __launch_bounds__(kJoinWaves* kWave) void embedding_join_kernel(LookGradArgs a, Sorted s, uint32_t slabs) {
+  const uint32_t n = *s.count, lane = threadIdx.x % kWave;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t items = *s.long_count * slabs;
+  for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const uint32_t start = s.long_runs[item / slabs], row = s.keys[start];
+    const uint32_t length = lower_bound(s.keys + start, n - start, row + 1);
+    const uint32_t col = item % slabs * kWave + lane;
+    const bool in = col < a.dim;
+    // the first fold's sum lies apart from the others', which stand two slots apart
+    float* const first = s.partials + partial_slot(start, true) * s.stride + col;
+    float* const rest = s.partials + partial_slot(start, false) * s.stride + col;
+    auto slot = [&](uint32_t fold) { return fold == 0 ? first : rest + 2 * (size_t)fold * s.stride; };
+    uint32_t level = 1;  // a level's sums stand in every level-th fold's slot
+    for (uint32_t sums = (length + kFold - 1) / kFold; sums > 1; sums = (sums + kFold - 1) / kFold) {
+      for (uint32_t g = wave; g * kFold < sums; g += kJoinWaves) {
+        const uint32_t from = g * kFold, count = sums - from < kFold ? sums - from : kFold;
+        if (in) {
+          float x[kFold];
+#pragma unroll
+          for (uint32_t i = 0; i < kFold; i++) x[i] = i < count ? *slot((from + i) * level) : 0.0f;
+          float v = x[0];
+#pragma unroll
+          for (uint32_t i = 1; i < kFold; i++) v = i < count ? v + x[i] : v;
+          *slot(from * level) = v;
+        }
       }
+      level *= kFold;
+      __syncthreads();
     }
-    level *= kFold;
-    __syncthreads();
+    if (wave == 0 && in) {
+      float v = *slot(0) * a.scale;
+      const size_t at = (size_t)row * a.dtable.stride + col;
+      if (a.accumulate) v = load_one<GT>(a.dtable.p, at) + v;
+      store_one<GT>(a.dtable.p, at, canon(v));
+    }
+    // a wavefront may go on to the next run: its sums lie elsewhere
   }
-  if (wave != 0 || left == 0) return;
-  const f4 v = *(const f4*)slot(0);
-  const float sum[4] = {v.x, v.y, v.z, v.w};
-  store_row<GT, 4>(a, row, col, left, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -506,6 +585,7 @@ hipError_t pick_look(const LookArgs& a, hipStream_t stream) {
 }
 
 hipError_t sort_tokens(const LookGradArgs& a, const LookGradLayout& l, Sorted* s, hipStream_t stream) {
+  s->named = a.accumulate ? nullptr : (uint8_t*)(a.workspace + l.named);
   uint32_t bits = 1;
   while (bits < 32 && ((a.vocab - 1) >> bits) != 0) bits++;
   Digits d;
@@ -518,16 +598,18 @@ hipError_t sort_tokens(const LookGradArgs& a, const LookGradLayout& l, Sorted* s
     tokens[i] = (uint32_t*)(a.workspace + l.tokens[i]);
   }
   s->count = count;
+  s->long_count = count + 1;
+  s->long_runs = (uint32_t*)(a.workspace + l.long_runs);
   if (a.tokens <= kSortSmall) {
     s->keys = keys[0], s->tokens = tokens[0];
-    sort_small_kernel<<<dim3(1), dim3(kSortThreads), 0, stream>>>(a, d, count, keys[0], tokens[0]);
+    sort_small_kernel<<<dim3(1), dim3(kSortThreads), 0, stream>>>(a, d, count, keys[0], tokens[0], s->named);
     return hipGetLastError();
   }
   const dim3 grid(sort_blocks(a.tokens));
   for (uint32_t pass = 0; pass < d.passes; pass++) {
     const int from = (pass + 1) % 2, to = pass % 2;
     DigitPass p = {pass == 0 ? nullptr : keys[from], tokens[from], count, (uint32_t*)(a.workspace + l.hist),
-                   pass * d.bits, d.bits};
+                   s->named, pass * d.bits, d.bits};
     sort_count_kernel<<<grid, dim3(kSortThreads), 0, stream>>>(a, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -540,21 +622,28 @@ hipError_t sort_tokens(const LookGradArgs& a, const LookGradLayout& l, Sorted* s
 
 template <int ET, int GT>
 hipError_t run_sums(const LookGradArgs& a, const Sorted& s, hipStream_t stream) {
-  constexpr size_t kCols = (size_t)kWave * Type<ET>::kVec;
-  const size_t slabs = (a.dim + kCols - 1) / kCols, units = look_windows(a.tokens) * slabs;
-  const size_t sums = (units + kSumWaves - 1) / kSumWaves;
-  // rows a workgroup looks after: about 256 KiB of the table, 64 at most
-  size_t each = ((size_t)256 << 10) / (a.dim * Type<GT>::kSize);
+  constexpr size_t kCols = Slab<ET, GT>::kCols;
+  const size_t slabs = (a.dim + kCols - 1) / kCols, units = (a.tokens + kWindow - 1) / kWindow * slabs;
+  const size_t sums = ((units + kSumWaves - 1) / kSumWaves + kXcds - 1) / kXcds * kXcds;
+  // rows a workgroup looks after: about 16 KiB of the table, 64 at most
+  size_t each = ((size_t)16 << 10) / (a.dim * Type<GT>::kSize);
   each = each < 1 ? 1 : each > 64 ? 64 : each;
-  const size_t zeros = a.accumulate ? 0 : (a.vocab + each - 1) / each;
-  if (sums + zeros > 0) {
-    embedding_sum_kernel<ET, GT><<<dim3((unsigned)(sums + zeros)), dim3(kSumWaves * kWave), 0, stream>>>(
-        a, s, (uint32_t)sums, (uint32_t)slabs, units, (uint32_t)each);
+  size_t zeros = a.accumulate ? 0 : (a.vocab + each - 1) / each;
+  zeros = (zeros + kXcds - 1) / kXcds * kXcds;
+  const dim3 grid((unsigned)(sums + zeros)), block(kSumWaves * kWave);
+  if (a.accumulate) {
+    embedding_sum_kernel<ET, GT, true><<<grid, block, 0, stream>>>(a, s, (uint32_t)sums, (uint32_t)slabs, units,
+                                                                   (uint32_t)each);
+  } else {
+    embedding_sum_kernel<ET, GT, false><<<grid, block, 0, stream>>>(a, s, (uint32_t)sums, (uint32_t)slabs, units,
+                                                                    (uint32_t)each);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.tokens <= kFold) return e;
-  const dim3 grid((unsigned)look_windows(a.tokens), (unsigned)((a.dim + 4 * kWave - 1) / (4 * kWave)));
-  embedding_join_kernel<GT><<<grid, dim3(kJoinWaves * kWave), 0, stream>>>(a, s);
+  // a long run has more than kFold tokens
+  const size_t join_slabs = (a.dim + kWave - 1) / kWave, items = a.tokens / (kFold + 1) * join_slabs;
+  embedding_join_kernel<GT><<<dim3((unsigned)(items < 2048 ? items : 2048)), dim3(kJoinWaves * kWave), 0, stream>>>(
+      a, s, (uint32_t)join_slabs);
   return hipGetLastError();
 }
 template <int ET>
@@ -575,7 +664,7 @@ hipError_t launch_embedding(const LookArgs& a, hipStream_t stream) {
 hipError_t launch_embedding_grad(const LookGradArgs& a, hipStream_t stream) {
   Sorted s = {};
   if (a.tokens > 0) {
-    const LookGradLayout l = look_grad_layout(a.tokens, a.dim);
+    const LookGradLayout l = look_grad_layout(a.tokens, a.vocab, a.dim);
     hipError_t e = sort_tokens(a, l, &s, stream);
     if (e != hipSuccess) return e;
     s.partials = (float*)(a.workspace + l.partials);

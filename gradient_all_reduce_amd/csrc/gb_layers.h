@@ -77,16 +77,18 @@ constexpr uint32_t kFold = 64;
 // Tokens that one workgroup sorts alone; more take a launch pair per digit.
 constexpr uint32_t kSortSmall = 8192;
 constexpr uint32_t kSortThreads = 1024;
-constexpr uint32_t kSortTile = 4096;    // tokens that a workgroup of the digit passes ranks at a time
-constexpr uint32_t kSortBlocks = 256;   // workgroups of a digit pass, at most
+constexpr uint32_t kSortTile = 2048;    // tokens that a workgroup of the digit passes ranks at a time
+constexpr uint32_t kSortBlocks = 128;   // workgroups of a digit pass, at most
 constexpr uint32_t kSortDigitBits = 10; // bins of a digit: one per lane of a workgroup
 
 // Byte offsets in the workspace of the embedding's backward pass.
 struct LookGradLayout {
-  size_t count;       // uint32: tokens that name a row
+  size_t count;       // uint32[2]: tokens that name a row, and runs of more than one fold
   size_t keys[2];     // uint32[tokens]: row of a token, and
   size_t tokens[2];   // uint32[tokens]: its number; two of each, a digit pass reads one and writes the other
   size_t hist;        // uint32[workgroups][bins] of a digit pass
+  size_t named;       // uint8[vocab]: whether a token names the row
+  size_t long_runs;   // uint32[tokens / (kFold + 1)]: where the runs of more than one fold begin
   size_t partials;    // float[2 * windows][stride]
   size_t total;
 };
@@ -96,7 +98,7 @@ inline uint32_t sort_blocks(size_t tokens) {
   const size_t tiles = (tokens + kSortTile - 1) / kSortTile;
   return (uint32_t)(tiles < kSortBlocks ? tiles : kSortBlocks);
 }
-inline LookGradLayout look_grad_layout(size_t tokens, size_t dim) {
+inline LookGradLayout look_grad_layout(size_t tokens, size_t vocab, size_t dim) {
   const auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   const bool digits = tokens > kSortSmall;
   LookGradLayout l;
@@ -107,6 +109,8 @@ inline LookGradLayout look_grad_layout(size_t tokens, size_t dim) {
     l.tokens[i] = at, at += i == 0 || digits ? up(4 * tokens) : 0;
   }
   l.hist = at, at += digits ? up((size_t)sort_blocks(tokens) * 4 << kSortDigitBits) : 0;
+  l.named = at, at += up(vocab);
+  l.long_runs = at, at += up(4 * (tokens / (kFold + 1)));
   l.partials = at, at += tokens > kFold ? up(2 * look_windows(tokens) * look_partial_stride(dim) * 4) : 0;
   l.total = at;
   return l;

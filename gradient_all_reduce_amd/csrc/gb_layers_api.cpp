@@ -310,7 +310,7 @@ gb_status gb_embedding_forward(int out_dtype, void* out, size_t out_stride, int 
 size_t gb_embedding_workspace_bytes(size_t tokens, size_t vocab, size_t dim) {
   if (tokens > GB_EMBEDDING_MAX_TOKENS || vocab > GB_EMBEDDING_MAX_VOCAB || dim > GB_EMBEDDING_MAX_DIM) return 0;
   if (tokens == 0 || vocab == 0 || dim == 0 || tokens > GB_MAX_N / dim || vocab > GB_MAX_N / dim) return 0;
-  return gb::look_grad_layout(tokens, dim).total;
+  return gb::look_grad_layout(tokens, vocab, dim).total;
 }
 
 gb_status gb_embedding_backward(int grad_dtype, void* dtable, size_t dtable_stride, size_t vocab, size_t dim,
