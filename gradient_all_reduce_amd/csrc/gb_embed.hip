@@ -268,11 +268,20 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(LookGradArgs
   // and after the earlier workgroups' tokens of the same bin.  With fewer bins
   // than lanes several lanes share the workgroups of a bin.
   uint32_t mine = 0, sum = 0;
-#pragma unroll 16
-  for (uint32_t b = threadIdx.x >> p.bits; b < gridDim.x; b += kSortThreads >> p.bits) {
-    const uint32_t c = p.hist[((size_t)b << p.bits) + bin];
-    if (b < blockIdx.x) mine += c;
-    sum += c;
+  const uint32_t sharers = kSortThreads >> p.bits;
+  for (uint32_t first = threadIdx.x >> p.bits; first < gridDim.x; first += 16 * sharers) {
+    uint32_t c[16];
+#pragma unroll
+    for (uint32_t i = 0; i < 16; i++) {
+      const uint32_t b = first + i * sharers;
+      c[i] = p.hist[((size_t)(b < gridDim.x ? b : 0) << p.bits) + bin];
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 16; i++) {
+      const uint32_t b = first + i * sharers;
+      if (b < blockIdx.x) mine += c[i];
+      if (b < gridDim.x) sum += c[i];
+    }
   }
   sums[0][threadIdx.x] = sum;
   sums[1][threadIdx.x] = mine;

@@ -442,8 +442,18 @@ __global__ __launch_bounds__(kJoinLanes* kSlices) void norm_join_kernel(NormGrad
   const float* const p = a.partials + blockIdx.y * a.partial_stride + col;
   f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
   if (col < a.cols) {
-#pragma unroll 4
-    for (uint32_t g = s; g < groups; g += kSlices) v += *(const f4*)(p + (size_t)g * 2 * a.partial_stride);
+    for (uint32_t first = s; first < groups; first += 4 * kSlices) {
+      f4 x[4];
+#pragma unroll
+      for (uint32_t i = 0; i < 4; i++) {
+        const uint32_t g = first + i * kSlices;
+        x[i] = *(const f4*)(p + (size_t)(g < groups ? g : s) * 2 * a.partial_stride);
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < 4; i++) {
+        if (first + i * kSlices < groups) v += x[i];
+      }
+    }
   }
   slice[s][l] = v;
   __syncthreads();
