@@ -711,18 +711,22 @@ _LAYER_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _ID_TYPES = {torch.int32: 6, torch.int64: 7}
 
 
+_F32, _BYTES = {torch.float32: 0}, {torch.uint8: 5}
+
+
 def _layer_tensor(t, device, name, types=_LAYER_TYPES):
     """gb_dtype number of a device tensor of one of types, on device if given."""
-    if isinstance(t, torch.Tensor):
-        number = types.get(t.dtype)
-        if number is not None and t.is_cuda and (device is None or t.get_device() == device):
-            return number
-        if number is None:
-            raise TypeError(f"{name} must be a tensor of one of {list(types)}, not {t.dtype}")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be in device memory, not on {t.device}")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    number = types.get(t.dtype)
+    if number is None:
+        raise TypeError(f"{name} must be a tensor of one of {list(types)}, not {t.dtype}")
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must be in device memory, not on {t.device}")
+    if device is not None and at != device:
         raise ValueError(f"{name} is on {t.device}, the first tensor on cuda:{device}")
-    raise TypeError(f"{name} must be a torch.Tensor")
+    return number
 
 
 def _matrix(t, name):
@@ -740,11 +744,13 @@ def _matrix(t, name):
     raise ValueError(f"{name} must be 2-D with adjacent values in a row, or contiguous")
 
 
-def _layer_matrix(t, device, name, dtype, rows, cols):
-    """(address, stride) of a rows x cols matrix of dtype."""
+def _layer_like(t, device, name, x, rows, cols):
+    """(address, stride) of a rows x cols matrix of x's type."""
+    if t is x:
+        return t.data_ptr(), _matrix(t, name)[2]
     _layer_tensor(t, device, name)
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dtype is not x.dtype:
+        raise TypeError(f"{name} must be {x.dtype}, not {t.dtype}")
     r, c, stride = _matrix(t, name)
     if r != rows or c != cols:
         raise ValueError(f"{name} has {r} rows of {c} values, expected {rows} of {cols}")
@@ -767,22 +773,53 @@ def _layer_pair(a, b, device, names, n):
     """Addresses of two vectors that share one element type, and its number
     (float32's without either)."""
     pa, ta = _layer_vector(a, device, names[0], n)
+    if b is None:
+        return pa, None, ta or 0
     pb, tb = _layer_vector(b, device, names[1], n)
-    if ta is not None and tb is not None and ta != tb:
+    if ta is not None and ta != tb:
         raise TypeError(f"{names[1]} must be {a.dtype} as {names[0]} is, not {b.dtype}")
-    return pa, pb, ta if ta is not None else tb if tb is not None else 0
+    return pa, pb, tb
+
+
+def _layer_stats(mean, rstd, device, rows):
+    """Addresses of the rows' statistics."""
+    if mean is None and rstd is None:
+        return None, None
+    return _layer_vector(mean, device, "mean", rows, _F32)[0], _layer_vector(rstd, device, "rstd", rows, _F32)[0]
 
 
 def _layer_workspace(workspace, device):
     if workspace is None:
         return None, 0
-    return _layer_vector(workspace, device, "workspace", workspace.numel(), _BYTES)[0], workspace.numel()
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    n = workspace.numel()
+    return _layer_vector(workspace, device, "workspace", n, _BYTES)[0], n
 
 
-_F32, _BYTES = {torch.float32: 0}, {torch.uint8: 5}
+def _layer_ids(ids, device):
+    """(address, gb_dtype, number) of the tokens' ids."""
+    number = _layer_tensor(ids, device, "ids", _ID_TYPES)
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    return ids.data_ptr(), number, ids.numel()
 
 
-def _layer_call(name, device, stream, *args):
+def _layer_rows(t, device, name, tokens, dim):
+    """(gb_dtype, address, stride) of a row of dim values for each token."""
+    number = _layer_tensor(t, device, name)
+    rows, cols, stride = _matrix(t, name)
+    if rows != tokens or cols != dim:
+        raise ValueError(f"{name} has {rows} rows of {cols} values, expected {tokens} of {dim}")
+    return number, t.data_ptr(), stride
+
+
+# the current device's number without torch.cuda's check for initialisation,
+# which a tensor on it makes needless; not every torch need have it
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _layer_call(call, device, stream, *args):
     """One library call on the device's current stream, or the one given, with
     the device current: the null stream's handle names no device."""
     if stream is not None:
@@ -791,13 +828,12 @@ def _layer_call(name, device, stream, *args):
         handle = _raw_stream(device)
     else:
         handle = torch.cuda.current_stream(device).cuda_stream
-    call = getattr(_lib, name)
-    if torch.cuda.current_device() == device:
+    if _current_device() == device:
         status = call(*args, handle)
     else:
         with torch.cuda.device(device):
             status = call(*args, handle)
-    if status != GB_OK:
+    if status:
         raise GbError(status, gb_last_error())
 
 
@@ -810,11 +846,10 @@ def gb_layer_norm_forward(y, x, weight=None, bias=None, eps=1e-5, mean=None, rst
     dtype = _layer_tensor(x, None, "x")
     device = x.get_device()
     rows, cols, x_stride = _matrix(x, "x")
-    y_ptr, y_stride = _layer_matrix(y, device, "y", x.dtype, rows, cols)
+    y_ptr, y_stride = _layer_like(y, device, "y", x, rows, cols)
     w, b, param = _layer_pair(weight, bias, device, ("weight", "bias"), cols)
-    _layer_call("gb_layer_norm_forward", device, stream, dtype, y_ptr, y_stride, x.data_ptr(), x_stride, rows, cols,
-                param, w, b, eps, _layer_vector(mean, device, "mean", rows, _F32)[0],
-                _layer_vector(rstd, device, "rstd", rows, _F32)[0])
+    _layer_call(_lib.gb_layer_norm_forward, device, stream, dtype, y_ptr, y_stride, x.data_ptr(), x_stride, rows, cols,
+                param, w, b, eps, *_layer_stats(mean, rstd, device, rows))
 
 
 def gb_layer_norm_workspace_bytes(rows, cols):
@@ -831,13 +866,12 @@ def gb_layer_norm_backward(dx, dweight, dbias, dy, x, mean, rstd, weight=None, a
     dtype = _layer_tensor(x, None, "x")
     device = x.get_device()
     rows, cols, x_stride = _matrix(x, "x")
-    dy_ptr, dy_stride = _layer_matrix(dy, device, "dy", x.dtype, rows, cols)
-    dx_ptr, dx_stride = (None, 0) if dx is None else _layer_matrix(dx, device, "dx", x.dtype, rows, cols)
+    dy_ptr, dy_stride = _layer_like(dy, device, "dy", x, rows, cols)
+    dx_ptr, dx_stride = (None, 0) if dx is None else _layer_like(dx, device, "dx", x, rows, cols)
     dw, db, grad = _layer_pair(dweight, dbias, device, ("dweight", "dbias"), cols)
     w, param = _layer_vector(weight, device, "weight", cols)
-    _layer_call("gb_layer_norm_backward", device, stream, dtype, dx_ptr, dx_stride, dy_ptr, dy_stride, x.data_ptr(),
-                x_stride, rows, cols, _layer_vector(mean, device, "mean", rows, _F32)[0],
-                _layer_vector(rstd, device, "rstd", rows, _F32)[0], param or 0, w, grad, dw, db,
+    _layer_call(_lib.gb_layer_norm_backward, device, stream, dtype, dx_ptr, dx_stride, dy_ptr, dy_stride, x.data_ptr(),
+                x_stride, rows, cols, *_layer_stats(mean, rstd, device, rows), param or 0, w, grad, dw, db,
                 1 if accumulate else 0, *_layer_workspace(workspace, device))
 
 
@@ -848,11 +882,10 @@ def gb_embedding_forward(out, table, ids, scale=1.0, first=0, stream=None):
     table_type = _layer_tensor(table, None, "table")
     device = table.get_device()
     vocab, dim, table_stride = _matrix(table, "table")
-    ids_ptr, id_type = _layer_vector(ids, device, "ids", ids.numel() if isinstance(ids, torch.Tensor) else 0, _ID_TYPES)
-    out_type = _layer_tensor(out, device, "out")
-    out_ptr, out_stride = _layer_matrix(out, device, "out", out.dtype, ids.numel(), dim)
-    _layer_call("gb_embedding_forward", device, stream, out_type, out_ptr, out_stride, table_type, table.data_ptr(),
-                table_stride, vocab, dim, id_type, ids_ptr, ids.numel(), first, scale)
+    ids_ptr, id_type, tokens = _layer_ids(ids, device)
+    out_type, out_ptr, out_stride = _layer_rows(out, device, "out", tokens, dim)
+    _layer_call(_lib.gb_embedding_forward, device, stream, out_type, out_ptr, out_stride, table_type, table.data_ptr(),
+                table_stride, vocab, dim, id_type, ids_ptr, tokens, first, scale)
 
 
 def gb_embedding_workspace_bytes(tokens, vocab, dim):
@@ -870,11 +903,10 @@ def gb_embedding_backward(dtable, dout, ids, scale=1.0, first=0, padding=-1, acc
     grad_type = _layer_tensor(dtable, None, "dtable")
     device = dtable.get_device()
     vocab, dim, dtable_stride = _matrix(dtable, "dtable")
-    ids_ptr, id_type = _layer_vector(ids, device, "ids", ids.numel() if isinstance(ids, torch.Tensor) else 0, _ID_TYPES)
-    dtype = _layer_tensor(dout, device, "dout")
-    dout_ptr, dout_stride = _layer_matrix(dout, device, "dout", dout.dtype, ids.numel(), dim)
-    _layer_call("gb_embedding_backward", device, stream, grad_type, dtable.data_ptr(), dtable_stride, vocab, dim,
-                dtype, dout_ptr, dout_stride, id_type, ids_ptr, ids.numel(), first, padding, scale,
+    ids_ptr, id_type, tokens = _layer_ids(ids, device)
+    dtype, dout_ptr, dout_stride = _layer_rows(dout, device, "dout", tokens, dim)
+    _layer_call(_lib.gb_embedding_backward, device, stream, grad_type, dtable.data_ptr(), dtable_stride, vocab, dim,
+                dtype, dout_ptr, dout_stride, id_type, ids_ptr, tokens, first, padding, scale,
                 1 if accumulate else 0, *_layer_workspace(workspace, device))
 
 
