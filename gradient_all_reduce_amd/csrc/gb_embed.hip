@@ -6,8 +6,20 @@
 namespace gb {
 namespace {
 
-__device__ __forceinline__ int64_t load_id(const void* ids, int dtype, size_t t) {
-  return dtype == GB_DTYPE_I64 ? *((const GB_GLOBAL int64_t*)ids + t) : (int64_t) * ((const GB_GLOBAL int32_t*)ids + t);
+// The ids of N tokens, one type test for all of them: a load inside a branch
+// would be waited for there.
+template <int N>
+__device__ __forceinline__ void load_ids(const void* ids, int dtype, const uint32_t (&token)[N], int64_t (&id)[N]) {
+  if (dtype == GB_DTYPE_I64) {
+#pragma unroll
+    for (int i = 0; i < N; i++) id[i] = ((const GB_GLOBAL int64_t*)ids)[token[i]];
+  } else {
+    int32_t narrow[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) narrow[i] = ((const GB_GLOBAL int32_t*)ids)[token[i]];
+#pragma unroll
+    for (int i = 0; i < N; i++) id[i] = narrow[i];
+  }
 }
 // The row of an id, or a number of vocab or more for an id outside the table:
 // the difference without a sign, which is at least 2^64 - 2^63 - first > vocab
@@ -16,37 +28,51 @@ __device__ __forceinline__ uint64_t row_of(int64_t id, int64_t first) { return (
 
 // ---------------------------------------------------------------------------
 // Lookup: the output is cut into vectors of V values, and a lane copies U of
-// them, 256 apart, all ids and then all rows in flight at once.
+// them, 256 apart, all ids and then all rows in flight at once: nothing is
+// read inside a branch, where it would be waited for (as it first was, with
+// each id and row guarded: 32,768 tokens of 4096 float32 values 131 us).  The
+// last vector of a row is moved back to end with the row, a token that names
+// no row reads the first one and stores zeros.  Rows shorter than a vector,
+// and a table without rows, take the guarded form.
 // ---------------------------------------------------------------------------
 constexpr int kLookThreads = 256;
-template <int TT, int OT, int U>
-__global__ __launch_bounds__(kLookThreads) void embedding_kernel(LookArgs a, uint32_t row_vecs, size_t vecs) {
-  constexpr int V = Type<TT>::kVec < Type<OT>::kVec ? Type<TT>::kVec : Type<OT>::kVec;
-  const size_t base = (size_t)blockIdx.x * (kLookThreads * U) + threadIdx.x;
-  size_t token[U];
-  uint64_t row[U];
-  uint32_t col[U];
-#pragma unroll
-  for (int u = 0; u < U; u++) {
-    const size_t v = base + (size_t)u * kLookThreads;
-    token[u] = v / row_vecs;
-    col[u] = (uint32_t)(v - token[u] * row_vecs) * V;
-    row[u] = v < vecs ? row_of(load_id(a.ids, a.id_dtype, token[u]), a.first) : a.vocab;
-  }
+struct LookCut {
+  uint32_t vecs;      // of this launch, 2^30 at most
+  uint32_t row_vecs;  // of a row
+  uint64_t inverse;   // 2^64 / row_vecs rounded up; 0 for row_vecs = 1
+};
+template <int TT, int OT, bool GUARDED>
+__global__ __launch_bounds__(kLookThreads) void embedding_kernel(LookArgs a, LookCut c) {
+  constexpr int V = Type<TT>::kVec < Type<OT>::kVec ? Type<TT>::kVec : Type<OT>::kVec, U = GUARDED ? 1 : 4;
+  const uint32_t dim = (uint32_t)a.dim, base = blockIdx.x * (kLookThreads * U) + threadIdx.x;
+  uint32_t token[U], col[U];
+  int64_t id[U];
+  bool in[U];
   Raw<TT, V> x[U];
 #pragma unroll
   for (int u = 0; u < U; u++) {
-    x[u] = row[u] < a.vocab ? load_raw<TT, V, false>(a.table.p, row[u] * a.table.stride + col[u],
-                                                     left_of(col[u], (uint32_t)a.dim))
-                            : zero_raw<TT, V>();
+    const uint32_t v = min(base + u * kLookThreads, c.vecs - 1);
+    // v / row_vecs: exact, as both are below 2^32
+    token[u] = c.inverse == 0 ? v : (uint32_t)__umul64hi(v, c.inverse);
+    col[u] = (v - token[u] * c.row_vecs) * V;
+    if constexpr (!GUARDED) col[u] = min(col[u], dim - V);
+  }
+  load_ids<U>(a.ids, a.id_dtype, token, id);
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    const uint64_t row = row_of(id[u], a.first);
+    in[u] = row < a.vocab;
+    const size_t at = (in[u] ? row : 0) * a.table.stride + col[u];
+    if constexpr (GUARDED) x[u] = load_raw<TT, V, false>(a.table.p, at, in[u] ? dim - col[u] : 0u);
+    else x[u] = load_full<TT, V, false>(a.table.p, at);
   }
 #pragma unroll
   for (int u = 0; u < U; u++) {
-    if (base + (size_t)u * kLookThreads >= vecs) break;
+    if (base + u * kLookThreads >= c.vecs) break;
     float y[V];
 #pragma unroll
-    for (int e = 0; e < V; e++) y[e] = row[u] < a.vocab ? canon(raw_value<TT, V>(x[u], e) * a.scale) : 0.0f;
-    store_vals<OT, V, true>(a.out.p, token[u] * a.out.stride + col[u], left_of(col[u], (uint32_t)a.dim), y);
+    for (int e = 0; e < V; e++) y[e] = in[u] ? canon(raw_value<TT, V>(x[u], e) * a.scale) : 0.0f;
+    store_vals<OT, V, true>(a.out.p, (size_t)token[u] * a.out.stride + col[u], GUARDED ? dim - col[u] : V, y);
   }
 }
 
@@ -63,11 +89,21 @@ struct Digits {
   uint32_t bits, passes;  // passes * bits cover vocab - 1
 };
 
-__device__ __forceinline__ bool token_row(const LookGradArgs& a, size_t t, uint32_t& row) {
-  const int64_t id = load_id(a.ids, a.id_dtype, t);
-  const uint64_t r = row_of(id, a.first);
-  row = (uint32_t)r;
-  return r < a.vocab && id != a.padding;
+// The rows of N tokens, those below `to` of them that name one marked valid.
+template <int N>
+__device__ __forceinline__ void token_rows(const LookGradArgs& a, const uint32_t (&token)[N], uint32_t to,
+                                           uint32_t (&key)[N], bool (&valid)[N]) {
+  uint32_t at[N];
+  int64_t id[N];
+#pragma unroll
+  for (int i = 0; i < N; i++) at[i] = min(token[i], (uint32_t)a.tokens - 1);
+  load_ids<N>(a.ids, a.id_dtype, at, id);
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    const uint64_t row = row_of(id[i], a.first);
+    valid[i] = token[i] < to && row < a.vocab && id[i] != a.padding;
+    key[i] = valid[i] ? (uint32_t)row : 0u;
+  }
 }
 
 // Lanes of the wavefront whose digit is this lane's, among the valid ones.
@@ -146,12 +182,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(LookGradArgs a
   uint32_t key[kSmallItems], token[kSmallItems], digit[kSmallItems], rank[kSmallItems];
   bool valid[kSmallItems];
   const uint32_t first = wave * rounds * kWave + lane;
+  // a wavefront's tokens end where the next one's begin
+  const uint32_t own_end = min((wave + 1) * rounds * kWave, (uint32_t)a.tokens);
 #pragma unroll
-  for (int i = 0; i < kSmallItems; i++) {
-    token[i] = first + i * kWave;
-    key[i] = 0;
-    valid[i] = i < (int)rounds && token[i] < a.tokens && token_row(a, token[i], key[i]);
-  }
+  for (int i = 0; i < kSmallItems; i++) token[i] = first + i * kWave;
+  token_rows<kSmallItems>(a, token, own_end, key, valid);
   uint32_t n = 0;
   if (named != nullptr) clear_named(a, named, 0, 1);
   for (uint32_t pass = 0; pass < d.passes; pass++) {
@@ -216,17 +251,29 @@ __device__ __forceinline__ size_t block_tokens(size_t tokens) {
   const size_t tiles = (tokens + kSortTile - 1) / kSortTile;
   return (tiles + gridDim.x - 1) / gridDim.x * kSortTile;
 }
-__device__ __forceinline__ bool pass_item(const LookGradArgs& a, const DigitPass& p, size_t at, size_t n,
-                                          uint32_t& key, uint32_t& token) {
-  if (at >= n) return false;
+// N items of a pass, those below `to` that name a row marked valid.
+template <int N>
+__device__ __forceinline__ void pass_items(const LookGradArgs& a, const DigitPass& p, const uint32_t (&at)[N],
+                                           uint32_t to, uint32_t (&key)[N], uint32_t (&token)[N], bool (&valid)[N]) {
   if (p.keys == nullptr) {
-    token = (uint32_t)at;
-    return token_row(a, at, key);
+    token_rows<N>(a, at, to, key, valid);
+#pragma unroll
+    for (int i = 0; i < N; i++) token[i] = at[i];
+    return;
   }
-  key = p.keys[at];
-  token = p.tokens[at];
-  return true;
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    const uint32_t j = min(at[i], (uint32_t)a.tokens - 1);
+    key[i] = p.keys[j];
+    token[i] = p.tokens[j];
+  }
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    valid[i] = at[i] < to;
+    key[i] = valid[i] ? key[i] : 0u;
+  }
 }
+constexpr int kTileItems = kSortTile / kSortThreads;
 
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(LookGradArgs a, DigitPass p) {
   __shared__ uint32_t bins[kBins];
@@ -235,15 +282,21 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(LookGradArgs a
   __syncthreads();
   const size_t n = p.keys == nullptr ? a.tokens : *p.count, each = block_tokens(a.tokens);
   const size_t from = blockIdx.x * each, to = from + each < n ? from + each : n;
-  for (size_t at = from + threadIdx.x; at < to; at += kSortThreads) {
-    uint32_t key, token;
-    if (pass_item(a, p, at, n, key, token)) atomicAdd(&bins[(key >> p.shift) & ((1u << p.bits) - 1u)], 1u);
+  for (size_t tile = from; tile < to; tile += kSortTile) {
+    uint32_t at[kTileItems], key[kTileItems], token[kTileItems];
+    bool valid[kTileItems];
+#pragma unroll
+    for (int i = 0; i < kTileItems; i++) at[i] = (uint32_t)tile + i * kSortThreads + threadIdx.x;
+    pass_items<kTileItems>(a, p, at, (uint32_t)to, key, token, valid);
+#pragma unroll
+    for (int i = 0; i < kTileItems; i++) {
+      if (valid[i]) atomicAdd(&bins[(key[i] >> p.shift) & ((1u << p.bits) - 1u)], 1u);
+    }
   }
   __syncthreads();
   if (threadIdx.x >> p.bits == 0) p.hist[((size_t)blockIdx.x << p.bits) + threadIdx.x] = bins[threadIdx.x];
 }
 
-constexpr int kTileItems = kSortTile / kSortThreads;
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(LookGradArgs a, DigitPass p, uint32_t* keys,
                                                                     uint32_t* tokens, uint32_t* count) {
   __shared__ uint16_t counts[kSortWaves][kBins];
@@ -256,12 +309,12 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(LookGradArgs
   uint32_t key[kTileItems], token[kTileItems], digit[kTileItems], rank[kTileItems];
   bool valid[kTileItems];
   auto load_tile = [&](size_t tile) {
+    uint32_t at[kTileItems];
 #pragma unroll
-    for (int i = 0; i < kTileItems; i++) {
-      key[i] = 0;
-      valid[i] = pass_item(a, p, tile + (wave * kTileItems + i) * kWave + lane, to, key[i], token[i]);
-      digit[i] = (key[i] >> p.shift) & ((1u << p.bits) - 1u);
-    }
+    for (int i = 0; i < kTileItems; i++) at[i] = (uint32_t)tile + (wave * kTileItems + i) * kWave + lane;
+    pass_items<kTileItems>(a, p, at, (uint32_t)to, key, token, valid);
+#pragma unroll
+    for (int i = 0; i < kTileItems; i++) digit[i] = (key[i] >> p.shift) & ((1u << p.bits) - 1u);
   };
   load_tile(from);
   // where this workgroup's tokens of each bin begin: after all smaller bins,
@@ -452,13 +505,17 @@ __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& 
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const uint32_t i = at + u < end ? at + u : end - 1;
-      const uint32_t t = i < 64 ? __builtin_amdgcn_readlane(token_a, i) : __builtin_amdgcn_readlane(token_b, i - 64);
-      x[u] = load_raw<ET, V, true>((const char*)a.dout.p + (size_t)t * a.dout.stride * Type<ET>::kSize, col, left);
-      if constexpr (ADD) {
-        if (i < 64 && ((whole >> i) & 1u)) {
-          const uint32_t row = __builtin_amdgcn_readlane(key_a, i);
-          old[u] = load_raw<GT, V, true>((const char*)a.dtable.p + (size_t)row * a.dtable.stride * Type<GT>::kSize, col,
-                                         left);
+      const uint32_t ta = __builtin_amdgcn_readlane(token_a, i % 64), tb = __builtin_amdgcn_readlane(token_b, i % 64);
+      const size_t t = i < 64 ? ta : tb;
+      x[u] = load_raw<ET, V, true>((const char*)a.dout.p + t * a.dout.stride * Type<ET>::kSize, col, left);
+    }
+    if constexpr (ADD) {
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const uint32_t i = at + u;
+        if (i < 64 && ((whole >> i) & 1u) && i < end) {
+          const size_t row = __builtin_amdgcn_readlane(key_a, i);
+          old[u] = load_raw<GT, V, true>((const char*)a.dtable.p + row * a.dtable.stride * Type<GT>::kSize, col, left);
         }
       }
     }
@@ -579,12 +636,26 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void embedding_join_kernel(LookG
 // Launches
 // ---------------------------------------------------------------------------
 template <int TT, int OT>
-hipError_t run_look(const LookArgs& a, hipStream_t stream) {
-  constexpr int V = Type<TT>::kVec < Type<OT>::kVec ? Type<TT>::kVec : Type<OT>::kVec, U = 4;
-  const size_t row_vecs = (a.dim + V - 1) / V, vecs = a.tokens * row_vecs;
-  const size_t grid = (vecs + kLookThreads * U - 1) / (kLookThreads * U);
-  embedding_kernel<TT, OT, U><<<dim3((unsigned)grid), dim3(kLookThreads), 0, stream>>>(a, (uint32_t)row_vecs, vecs);
-  return hipGetLastError();
+hipError_t run_look(LookArgs a, hipStream_t stream) {
+  constexpr int V = Type<TT>::kVec < Type<OT>::kVec ? Type<TT>::kVec : Type<OT>::kVec;
+  const bool guarded = a.dim < V || a.vocab == 0;
+  LookCut c;
+  c.row_vecs = (uint32_t)((a.dim + V - 1) / V);
+  c.inverse = c.row_vecs == 1 ? 0 : ~(uint64_t)0 / c.row_vecs + 1;
+  // a launch takes as many tokens as 2^30 vectors hold
+  const size_t most = ((size_t)1 << 30) / c.row_vecs, tokens = a.tokens, each = kLookThreads * (guarded ? 1 : 4);
+  for (size_t t = 0; t < tokens; t += most) {
+    const size_t now = tokens - t < most ? tokens - t : most;
+    c.vecs = (uint32_t)(now * c.row_vecs);
+    const dim3 grid((unsigned)((c.vecs + each - 1) / each));
+    if (guarded) embedding_kernel<TT, OT, true><<<grid, dim3(kLookThreads), 0, stream>>>(a, c);
+    else embedding_kernel<TT, OT, false><<<grid, dim3(kLookThreads), 0, stream>>>(a, c);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.ids = (const char*)a.ids + now * (a.id_dtype == GB_DTYPE_I64 ? 8 : 4);
+    a.out.p = (char*)a.out.p + now * a.out.stride * Type<OT>::kSize;
+  }
+  return hipSuccess;
 }
 template <int TT>
 hipError_t pick_look(const LookArgs& a, hipStream_t stream) {
