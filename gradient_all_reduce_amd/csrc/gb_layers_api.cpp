@@ -184,7 +184,8 @@ gb_status check_ids(const void* ids, int id_dtype, size_t tokens, size_t vocab, 
   GB_TRY(check_shape(tokens, dim, fn, "tokens", "dim"));
   GB_TRY(check_shape(vocab, dim, fn, "vocab", "dim"));
   if (first > INT64_MAX - (int64_t)vocab) {  // an id's distance from first, without a sign, then names one row
-    return fail(GB_ERR_INVALID_ARG, "%s: first = %lld and vocab = %zu pass the largest id", fn, (long long)first, vocab);
+    return fail(GB_ERR_INVALID_ARG, "%s: first = %lld and vocab = %zu pass the largest id", fn, (long long)first,
+                vocab);
   }
   if (id_dtype != GB_DTYPE_I32 && id_dtype != GB_DTYPE_I64) {
     return fail(GB_ERR_UNSUPPORTED, "%s: id_dtype = %d is not int32 or int64", fn, id_dtype);

@@ -280,7 +280,8 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
     auto terms = [&](int k, float (&hk)[V], float (&gk)[V]) {
 #pragma unroll
       for (int j = 0; j < V; j += 4) {
-        const f4 wj = kWeightsInLds ? lds_w[(k * V + j) / 4][threadIdx.x] : f4{w[k][j], w[k][j + 1], w[k][j + 2], w[k][j + 3]};
+        f4 wj = {w[k][j], w[k][j + 1], w[k][j + 2], w[k][j + 3]};
+        if constexpr (kWeightsInLds) wj = lds_w[(k * V + j) / 4][threadIdx.x];
 #pragma unroll
         for (int e = j; e < j + 4; e++) {
           hk[e] = (raw_value<ET, V>(now.x[k], e) - m) * s;
