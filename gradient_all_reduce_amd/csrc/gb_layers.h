@@ -79,7 +79,8 @@ constexpr uint32_t kSortSmall = 8192;
 constexpr uint32_t kSortThreads = 1024;
 constexpr uint32_t kSortTile = 2048;    // tokens that a workgroup of the digit passes ranks at a time
 constexpr uint32_t kSortBlocks = 128;   // workgroups of a digit pass, at most
-constexpr uint32_t kSortDigitBits = 10; // bins of a digit: one per lane of a workgroup
+constexpr uint32_t kSortDigitBits = 10; // bins of a digit: one per lane of a workgroup, at most
+constexpr uint32_t kSortLeastBits = 8;  // and at least 256, or few lanes add up many lanes' counts
 
 // Byte offsets in the workspace of the embedding's backward pass.
 struct LookGradLayout {

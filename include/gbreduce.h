@@ -749,8 +749,8 @@ gb_status gb_adamw_step(const gb_optim_handle* plan, const void* control, void* 
  * and the parameters and gradients need only the alignment of their element:
  * all may be views.  For the overlap rule an array reaches from its first
  * value to its last, the gaps between its rows included.  Types are
- * GB_DTYPE_F32, F16 or BF16 each; arithmetic is binary32, and an output is
- * rounded to its type once.  Every NaN is stored as 0x7FC00000, or as that
+ * GB_DTYPE_F32, F16 or BF16 each; arithmetic is binary32 (the layer norm's with
+ * fused multiply-adds), and an output is rounded to its type once.  Every NaN is stored as 0x7FC00000, or as that
  * NaN's rounding.  Calls with different workspaces may run at the same time;
  * two that share one belong on one stream, or ordered by events.
  * ------------------------------------------------------------------------- */
@@ -768,8 +768,8 @@ gb_status gb_adamw_step(const gb_optim_handle* plan, const void* control, void* 
  *   mean, rstd  float[rows], written for the backward pass; NULL: not stored
  * cols 1 .. GB_NORM_MAX_COLS; eps finite and above 0 in binary32.  rows == 0
  * is GB_OK and enqueues nothing.  Forward and backward results agree with the
- * formulas up to the binary32 roundings of their sums (not fixed bit for bit
- * across versions of this library, as the codecs are).
+ * formulas up to the binary32 roundings of their sums; unlike the codecs' they
+ * are not fixed bit for bit across versions of this library.
  */
 gb_status gb_layer_norm_forward(int dtype, void* y, size_t y_stride, const void* x, size_t x_stride, size_t rows,
                                 size_t cols, int param_dtype, const void* weight, const void* bias, double eps,
