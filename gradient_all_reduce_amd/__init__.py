@@ -805,6 +805,13 @@ def _layer_ids(ids, device):
     return ids.data_ptr(), number, ids.numel()
 
 
+def _layer_id(v, name):
+    """An id as the library's int64, which ctypes would wrap silently."""
+    if not -(1 << 63) <= v < 1 << 63:
+        raise ValueError(f"{name} = {v} is no 64-bit id")
+    return v
+
+
 def _layer_rows(t, device, name, tokens, dim):
     """(gb_dtype, address, stride) of a row of dim values for each token."""
     number = _layer_tensor(t, device, name)
@@ -885,7 +892,7 @@ def gb_embedding_forward(out, table, ids, scale=1.0, first=0, stream=None):
     ids_ptr, id_type, tokens = _layer_ids(ids, device)
     out_type, out_ptr, out_stride = _layer_rows(out, device, "out", tokens, dim)
     _layer_call(_lib.gb_embedding_forward, device, stream, out_type, out_ptr, out_stride, table_type, table.data_ptr(),
-                table_stride, vocab, dim, id_type, ids_ptr, tokens, first, scale)
+                table_stride, vocab, dim, id_type, ids_ptr, tokens, _layer_id(first, "first"), scale)
 
 
 def gb_embedding_workspace_bytes(tokens, vocab, dim):
@@ -906,8 +913,8 @@ def gb_embedding_backward(dtable, dout, ids, scale=1.0, first=0, padding=-1, acc
     ids_ptr, id_type, tokens = _layer_ids(ids, device)
     dtype, dout_ptr, dout_stride = _layer_rows(dout, device, "dout", tokens, dim)
     _layer_call(_lib.gb_embedding_backward, device, stream, grad_type, dtable.data_ptr(), dtable_stride, vocab, dim,
-                dtype, dout_ptr, dout_stride, id_type, ids_ptr, tokens, first, padding, scale,
-                1 if accumulate else 0, *_layer_workspace(workspace, device))
+                dtype, dout_ptr, dout_stride, id_type, ids_ptr, tokens, _layer_id(first, "first"),
+                _layer_id(padding, "padding"), scale, 1 if accumulate else 0, *_layer_workspace(workspace, device))
 
 
 def gb_payload_bytes(codec, n):

@@ -7,11 +7,11 @@
 // 6.69: 32,768 tokens out of a 131,072 x 4096 float32 table into bfloat16 95 us
 // (4.9 TB/s by the bytes of the different rows, 197 MB; rows are read again for each
 // of their tokens, 537 MB, and 367 MB of that pass the L2s); the gradient of 16,384 bfloat16
-// tokens written over all of a 131,072 x 4096 float32 table 416 to 440 us (5.2 to
-// 5.5 TB/s: the sums and zeros 393 to 406 us, the sort 27, the join 8), of 98,304
-// tokens added into 50,003 x 1024 110 to 125 us (3.0 to 3.3 TB/s: the sums 76 to 82,
-// the sort 26, the join 8 to 12), of 512 tokens over 2000 x 257 float32 values 9 us
-// the sort, 9 the sums and 4 the join.
+// tokens written over all of a 131,072 x 4096 float32 table 414 to 435 us (5.2 to
+// 5.5 TB/s: the sums and zeros 378 to 393 us, the sort 27, the join 6), of 98,304
+// tokens added into 50,003 x 1024 106 to 118 us (3.1 to 3.5 TB/s: the sums 74 to 79,
+// the sort 26, the join 6 to 10), of 512 tokens over 2000 x 257 float32 values 9 us
+// the sort, 9 the sums and 2 the join.
 #include "gb_rows.h"
 
 namespace gb {
@@ -130,9 +130,9 @@ __device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
-// Ranks `items` (I at most) digits a lane within the wavefront, item i of the lanes before item
-// i + 1: rank[i] counts the equal digits before it, and counts[digit] ends as
-// their number.  counts: zeroed, this wavefront's own.
+// Ranks `items` (I at most) digits a lane within the wavefront, item i of the
+// lanes before item i + 1: rank[i] counts the equal digits before it, and
+// counts[digit] ends as their number.  counts: zeroed, this wavefront's own.
 template <int I>
 __device__ __forceinline__ void rank_wave(const uint32_t (&digit)[I], const bool (&valid)[I], uint32_t items,
                                           uint32_t bits, volatile uint16_t* counts, uint32_t (&rank)[I]) {
@@ -412,10 +412,14 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(LookGradArgs
 constexpr uint32_t kWindow = 16;
 static_assert(kFold % kWindow == 0 && kFold == kWave, "a fold is a lane each");
 
+struct LongRun {
+  uint32_t start, length, row;
+};
+static_assert(sizeof(LongRun) == kLongRunBytes, "the workspace has room for them");
 struct Sorted {
   uint32_t* count;       // tokens that name a row; NULL: no tokens
-  uint32_t* long_count;  // runs of more than one fold, and where they begin
-  uint32_t* long_runs;
+  uint32_t* long_count;  // runs of more than one fold
+  LongRun* long_runs;
   const uint32_t* keys;
   const uint32_t* tokens;
   float* partials;
@@ -489,11 +493,20 @@ __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& 
   // where runs begin in the lanes' tokens, and whether one goes on into them
   const uint64_t starts = __ballot(pa < n && (pa == 0 || before != key_a));
   uint64_t heads = starts;
+  // runs of more than one fold from here on
+  const uint64_t more = __ballot(pb < n && key_b == key_a);
   if (!(starts & 1u)) {
     const uint32_t key = __builtin_amdgcn_readfirstlane(key_a);
-    const uint32_t offset = (lower_bound(s.keys, p0, key) - p0) % kFold;  // of its next fold from here
-    const uint64_t same = __ballot(pa < n && key_a == key);
-    if ((same >> offset) & 1u) heads |= (uint64_t)1 << offset;
+    const uint32_t start = lower_bound(s.keys, p0, key), offset = (start - p0) % kFold;  // of its next fold from here
+    const uint64_t same = __ballot(pa < n && key_a == key), rest = __ballot(pb < n && key_b == key);
+    if ((same >> offset) & 1u) {
+      heads |= (uint64_t)1 << offset;
+      if (slab == 0 && lane == 0 && offset < kWindow && !((more >> offset) & 1u)) {
+        // the run's last fold: the run goes to the join's work list, whose order changes no result
+        const uint32_t end = p0 + __popcll(same) + (same == ~(uint64_t)0 ? __popcll(rest) : 0);
+        s.long_runs[atomicAdd(s.long_count, 1u)] = LongRun{start, end - start, key};
+      }
+    }
   }
   heads &= ((uint64_t)1 << kWindow) - 1;
   if (heads == 0) return;
@@ -503,13 +516,7 @@ __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& 
   const uint64_t tail_a = __ballot(pa < n && key_a == last_key) >> last;
   const uint64_t tail_b = __ballot(pb < n && key_b == last_key && lane < last);
   const uint32_t end = last + __popcll(tail_a) + __popcll(tail_b);
-  // runs of more than one fold
-  const uint64_t more = __ballot(pb < n && key_b == key_a);
   const uint64_t whole = starts & ~more;  // runs of one fold: their sums are the table's
-  if (slab == 0 && lane < kWindow && ((starts & more) >> lane & 1u)) {
-    // the join's work list; its order changes no result
-    s.long_runs[atomicAdd(s.long_count, 1u)] = pa;
-  }
 
   float acc[V];
   Raw<ET, V> x[U];
@@ -605,19 +612,18 @@ __global__ __launch_bounds__(kSumWaves* kWave) void embedding_sum_kernel(LookGra
 }
 
 // The sums of runs of several folds (a grid over all windows instead of the work
-// list takes 22 us where this takes 12): a workgroup takes a run of the work list
+// list takes 22 us where this takes 6 to 10): a workgroup takes a run of the work list
 // for a slab of 64 columns at a time.  Level by level kFold sums are added in
 // order, each wavefront taking every kJoinWaves-th of a level's groups, all of
 // a group's loads in flight at once.
 constexpr int kJoinWaves = 4;
 template <int GT>
 __global__ __launch_bounds__(kJoinWaves* kWave) void embedding_join_kernel(LookGradArgs a, Sorted s, uint32_t slabs) {
-  const uint32_t n = *s.count, lane = threadIdx.x % kWave;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t items = *s.long_count * slabs;
   for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const uint32_t start = s.long_runs[item / slabs], row = s.keys[start];
-    const uint32_t length = lower_bound(s.keys + start, n - start, row + 1);
+    const LongRun run = s.long_runs[item / slabs];
+    const uint32_t start = run.start, length = run.length, row = run.row;
     const uint32_t col = item % slabs * kWave + lane;
     const bool in = col < a.dim;
     // the first fold's sum lies apart from the others', which stand two slots apart
@@ -699,7 +705,7 @@ hipError_t sort_tokens(const LookGradArgs& a, const LookGradLayout& l, Sorted* s
   }
   s->count = count;
   s->long_count = count + 1;
-  s->long_runs = (uint32_t*)(a.workspace + l.long_runs);
+  s->long_runs = (LongRun*)(a.workspace + l.long_runs);
   if (a.tokens <= kSortSmall) {
     s->keys = keys[0], s->tokens = tokens[0];
     sort_small_kernel<<<dim3(1), dim3(kSortThreads), 0, stream>>>(a, d, count, keys[0], tokens[0], s->named);

@@ -74,6 +74,9 @@ hipError_t launch_embedding(const LookArgs& a, hipStream_t stream);
 // are added in turn: the unit of the sum's order that the ABI documents.
 constexpr uint32_t kFold = 64;
 
+// A run of more than one fold in the join's work list.
+constexpr size_t kLongRunBytes = 12;
+
 // Tokens that one workgroup sorts alone; more take a launch pair per digit.
 constexpr uint32_t kSortSmall = 8192;
 constexpr uint32_t kSortThreads = 1024;
@@ -89,7 +92,7 @@ struct LookGradLayout {
   size_t tokens[2];   // uint32[tokens]: its number; two of each, a digit pass reads one and writes the other
   size_t hist;        // uint32[workgroups][bins] of a digit pass
   size_t named;       // uint8[vocab]: whether a token names the row
-  size_t long_runs;   // uint32[tokens / (kFold + 1)]: where the runs of more than one fold begin
+  size_t long_runs;   // kLongRunBytes[tokens / (kFold + 1)]: the runs of more than one fold
   size_t partials;    // float[2 * windows][stride]
   size_t total;
 };
@@ -111,7 +114,7 @@ inline LookGradLayout look_grad_layout(size_t tokens, size_t vocab, size_t dim) 
   }
   l.hist = at, at += digits ? up((size_t)sort_blocks(tokens) * 4 << kSortDigitBits) : 0;
   l.named = at, at += up(vocab);
-  l.long_runs = at, at += up(4 * (tokens / (kFold + 1)));
+  l.long_runs = at, at += up(kLongRunBytes * (tokens / (kFold + 1)));
   l.partials = at, at += tokens > kFold ? up(2 * look_windows(tokens) * look_partial_stride(dim) * 4) : 0;
   l.total = at;
   return l;

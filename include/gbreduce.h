@@ -829,8 +829,9 @@ size_t gb_embedding_workspace_bytes(size_t tokens, size_t vocab, size_t dim);
 /*
  * gb_embedding_backward — the table's gradient, from dout (that of out):
  *   dtable[r][i] = [dtable[r][i] +] RN(scale * S(dout[t][i] over the tokens t with ids[t] - first == r))
- * the term in brackets with accumulate == 1.  A token whose id is `padding`
- * (-1: none, where no id is) or outside the shard is left out.  Without
+ * the term in brackets with accumulate == 1.  A token whose id is `padding` or
+ * outside the shard is left out (-1 for no padding; a negative first makes -1
+ * an id like any other, and padding then has to lie outside the shard).  Without
  * accumulate every row is written, those without a token with zeros; with it
  * only the rows that tokens name are read and written.
  * S adds in binary32 in the order of the tokens, 64 at a time: the first 64

@@ -102,7 +102,7 @@ hipError_t launch_embedding_grad(const LookGradArgs& a, hipStream_t) {
                         {l.tokens[1], digits ? 4 * a.tokens : 0},
                         {l.hist, digits ? ((size_t)sort_blocks(a.tokens) * 4 << kSortDigitBits) : 0},
                         {l.named, (a.vocab + 15) / 16 * 16},
-                        {l.long_runs, 4 * (a.tokens / (kFold + 1))},
+                        {l.long_runs, kLongRunBytes * (a.tokens / (kFold + 1))},
                         {l.partials, a.tokens > kFold ? 8 * look_windows(a.tokens) * look_partial_stride(a.dim) : 0}};
   int mark = 1;
   for (const Part& p : parts) std::memset(a.workspace + p.at, mark++, p.bytes);

@@ -190,6 +190,8 @@ def test_the_binding_refuses_shapes_types_and_devices_that_do_not_match(gb):
         (lambda: gb.gb_embedding_forward(x, x, On(torch, (4,), i, 1)), ValueError, "ids is on"),
         (lambda: gb.gb_embedding_backward(x, On(torch, (4, 7), f), On(torch, (4,), i)), ValueError, "dout has"),
         (lambda: gb.gb_embedding_backward(x, x, On(torch, (4,), i, 0, (2,))), ValueError, "ids must be contiguous"),
+        (lambda: gb.gb_embedding_forward(x, x, On(torch, (4,), i), first=1 << 63), ValueError, "first = .* 64-bit"),
+        (lambda: gb.gb_embedding_backward(x, x, On(torch, (4,), i), padding=-(1 << 63) - 1), ValueError, "padding ="),
     ]
     for call, error, text in cases:
         with pytest.raises(error, match=text):
