@@ -8,10 +8,10 @@
 // (4.9 TB/s by the bytes of the different rows, 197 MB; rows are read again for each
 // of their tokens, 537 MB, and 367 MB of that pass the L2s); the gradient of 16,384 bfloat16
 // tokens written over all of a 131,072 x 4096 float32 table 414 to 435 us (5.2 to
-// 5.5 TB/s: the sums and zeros 378 to 393 us, the sort 27, the join 6), of 98,304
-// tokens added into 50,003 x 1024 106 to 118 us (3.1 to 3.5 TB/s: the sums 74 to 79,
-// the sort 26, the join 6 to 10), of 512 tokens over 2000 x 257 float32 values 9 us
-// the sort, 9 the sums and 2 the join.
+// 5.5 TB/s: the sums and zeros 375 to 395 us, the sort 26, the join 6), of 98,304
+// tokens added into 50,003 x 1024 105 to 118 us (3.1 to 3.5 TB/s: the sums 72 to 76,
+// the sort 25, the join 6 to 10), of 512 tokens over 2000 x 257 float32 values 9 us
+// the sort, 8 the sums and 2 the join.
 #include "gb_rows.h"
 
 namespace gb {
@@ -119,12 +119,16 @@ __device__ __forceinline__ void token_rows(const LookGradArgs& a, const uint32_t
 
 // Lanes of the wavefront whose digit is this lane's, among the valid ones.
 __device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool valid, uint32_t bits) {
-  uint64_t same = __ballot(valid);
+  const uint64_t all = __ballot(valid);
+  uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
+#pragma unroll 2
   for (uint32_t b = 0; b < bits; b++) {
-    const uint64_t set = __ballot((digit >> b) & 1u);
-    same &= (digit >> b) & 1u ? set : ~set;
+    const uint32_t mine = 0u - ((digit >> b) & 1u);  // all ones, or zeros
+    const uint64_t set = __ballot(mine != 0u);
+    lo &= ~((uint32_t)set ^ mine);
+    hi &= ~((uint32_t)(set >> 32) ^ mine);
   }
-  return same;
+  return (uint64_t)hi << 32 | lo;
 }
 __device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
@@ -541,11 +545,35 @@ __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& 
         }
       }
     }
+    // the sum of the fold that ends before token i, to where it belongs
+    auto ends_before = [&](uint32_t i) { return i == end || (i < kWindow && ((heads >> i) & 1u)); };
+    auto store_fold = [&]() {
+      if ((whole >> head) & 1u) {
+        store_row<GT, V, ADD>(a, __builtin_amdgcn_readlane(key_a, head), col, left, acc, now);
+      } else {
+        float* const out = s.partials + partial_slot(p0 + head, (starts >> head) & 1u) * s.stride;
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+          const float v[4] = {acc[j], acc[j + 1], acc[j + 2], acc[j + 3]};
+          store_vals<GB_DTYPE_F32, 4, false>(out, col + j, left > (uint32_t)j ? left - j : 0u, v);
+        }
+      }
+    };
+    if (at + U <= end && (at >= kWindow || ((heads >> at) & ((1u << U) - 1u)) == 0)) {
+      // within a fold: nothing but additions
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+#pragma unroll
+        for (int e = 0; e < V; e++) acc[e] += raw_value<ET, V>(x[u], e);
+      }
+      if (ends_before(at + U)) store_fold();
+      continue;
+    }
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const uint32_t i = at + u;
       if (i >= end) break;
-      const bool begins = i < 64 && ((heads >> i) & 1u);
+      const bool begins = i < kWindow && ((heads >> i) & 1u);
       if (begins) {
         head = i;
         if constexpr (ADD) now = old[u];
@@ -555,18 +583,7 @@ __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& 
         const float v = raw_value<ET, V>(x[u], e);
         acc[e] = begins ? v : acc[e] + v;
       }
-      if (i + 1 == end || (i + 1 < 64 && ((heads >> (i + 1)) & 1u))) {
-        if ((whole >> head) & 1u) {
-          store_row<GT, V, ADD>(a, __builtin_amdgcn_readlane(key_a, head), col, left, acc, now);
-        } else {
-          float* const out = s.partials + partial_slot(p0 + head, (starts >> head) & 1u) * s.stride;
-#pragma unroll
-          for (int j = 0; j < V; j += 4) {
-            const float v[4] = {acc[j], acc[j + 1], acc[j + 2], acc[j + 3]};
-            store_vals<GB_DTYPE_F32, 4, false>(out, col + j, left > (uint32_t)j ? left - j : 0u, v);
-          }
-        }
-      }
+      if (ends_before(i + 1)) store_fold();
     }
   }
 }
