@@ -7,11 +7,11 @@
 // 6.69: 32,768 tokens out of a 131,072 x 4096 float32 table into bfloat16 95 us
 // (4.9 TB/s by the bytes of the different rows, 197 MB; rows are read again for each
 // of their tokens, 537 MB, and 367 MB of that pass the L2s); the gradient of 16,384 bfloat16
-// tokens written over all of a 131,072 x 4096 float32 table 414 to 435 us (5.2 to
-// 5.5 TB/s: the sums and zeros 375 to 395 us, the sort 26, the join 6), of 98,304
-// tokens added into 50,003 x 1024 105 to 118 us (3.1 to 3.5 TB/s: the sums 72 to 76,
+// tokens written over all of a 131,072 x 4096 float32 table 413 to 436 us (5.2 to
+// 5.5 TB/s: the sums and zeros 375 to 405 us, the sort 26, the join 6), of 98,304
+// tokens added into 50,003 x 1024 105 to 122 us (3.0 to 3.5 TB/s: the sums 72 to 82,
 // the sort 25, the join 6 to 10), of 512 tokens over 2000 x 257 float32 values 9 us
-// the sort, 8 the sums and 2 the join.
+// the sort, 8 the sums and 2 to 4 the join.
 #include "gb_rows.h"
 
 namespace gb {
