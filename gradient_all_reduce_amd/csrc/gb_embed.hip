@@ -479,6 +479,7 @@ __device__ __forceinline__ void store_row(const LookGradArgs& a, uint32_t row, u
 
 constexpr int kSumWaves = 4;
 constexpr uint32_t kXcds = 8;
+static_assert(kSumLaunch % kXcds == 0 && (uint64_t)kSumLaunch * kSumWaves * kWave < (uint64_t)1 << 32, "a launch's lanes");
 template <int ET, int GT, bool ADD, bool FULL>
 __device__ __forceinline__ void sum_window(const LookGradArgs& a, const Sorted& s, uint32_t window, uint32_t slab) {
   constexpr int V = Slab<ET, GT>::V, U = 8;
@@ -612,19 +613,18 @@ __device__ __forceinline__ void zero_rows(const LookGradArgs& a, const Sorted& s
 
 // Workgroups [0, sums) take windows and slabs, the rest rows without a token.
 template <int ET, int GT, bool ADD>
-__global__ __launch_bounds__(kSumWaves* kWave) void embedding_sum_kernel(LookGradArgs a, Sorted s, uint32_t sums,
-                                                                        uint32_t slabs, size_t units,
-                                                                        uint32_t zero_each) {
-  if (ADD || blockIdx.x < sums) {
-    const size_t unit = (size_t)blockIdx.x * kSumWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    if (unit >= units) return;
-    const uint32_t window = (uint32_t)(unit / slabs), slab = (uint32_t)(unit % slabs);
+__global__ __launch_bounds__(kSumWaves* kWave) void embedding_sum_kernel(LookGradArgs a, Sorted s, SumGrid g) {
+  const uint32_t group = g.base + blockIdx.x;
+  if (ADD || group < g.sums) {
+    const size_t unit = (size_t)group * kSumWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if (unit >= g.units) return;
+    const uint32_t window = (uint32_t)(unit / g.slabs), slab = (uint32_t)(unit % g.slabs);
     if ((slab + 1) * Slab<ET, GT>::kCols <= a.dim) sum_window<ET, GT, ADD, true>(a, s, window, slab);
     else sum_window<ET, GT, ADD, false>(a, s, window, slab);
   } else {
     // workgroups go to the 8 XCDs in turn: each XCD's rows lie together
-    const uint32_t z = blockIdx.x - sums, per_xcd = (gridDim.x - sums) / kXcds;
-    zero_rows<GT>(a, s, ((size_t)(z % kXcds) * per_xcd + z / kXcds) * zero_each, zero_each);
+    const uint32_t z = group - g.sums, per_xcd = g.zeros / kXcds;
+    zero_rows<GT>(a, s, ((size_t)(z % kXcds) * per_xcd + z / kXcds) * g.zero_each, g.zero_each);
   }
 }
 
@@ -746,23 +746,22 @@ hipError_t sort_tokens(const LookGradArgs& a, const LookGradLayout& l, Sorted* s
 template <int ET, int GT>
 hipError_t run_sums(const LookGradArgs& a, const Sorted& s, hipStream_t stream) {
   constexpr size_t kCols = Slab<ET, GT>::kCols;
-  const size_t slabs = (a.dim + kCols - 1) / kCols, units = (a.tokens + kWindow - 1) / kWindow * slabs;
-  const size_t sums = ((units + kSumWaves - 1) / kSumWaves + kXcds - 1) / kXcds * kXcds;
+  SumGrid g = {};
+  g.slabs = (uint32_t)((a.dim + kCols - 1) / kCols);
+  g.units = (a.tokens + kWindow - 1) / kWindow * g.slabs;
+  g.sums = (uint32_t)(((g.units + kSumWaves - 1) / kSumWaves + kXcds - 1) / kXcds * kXcds);
   // rows a workgroup looks after (zero_rows): about 16 KiB of the table, 64 at most
-  size_t each = ((size_t)16 << 10) / (a.dim * Type<GT>::kSize);
-  each = each < 1 ? 1 : each > 64 ? 64 : each;
-  size_t zeros = a.accumulate ? 0 : (a.vocab + each - 1) / each;
-  zeros = (zeros + kXcds - 1) / kXcds * kXcds;
-  const dim3 grid((unsigned)(sums + zeros)), block(kSumWaves * kWave);
-  if (a.accumulate) {
-    embedding_sum_kernel<ET, GT, true><<<grid, block, 0, stream>>>(a, s, (uint32_t)sums, (uint32_t)slabs, units,
-                                                                   (uint32_t)each);
-  } else {
-    embedding_sum_kernel<ET, GT, false><<<grid, block, 0, stream>>>(a, s, (uint32_t)sums, (uint32_t)slabs, units,
-                                                                    (uint32_t)each);
+  const size_t each = ((size_t)16 << 10) / (a.dim * Type<GT>::kSize);
+  g.zero_each = each < 1 ? 1 : each > 64 ? 64 : (uint32_t)each;
+  if (!a.accumulate) g.zeros = (uint32_t)(((a.vocab + g.zero_each - 1) / g.zero_each + kXcds - 1) / kXcds * kXcds);
+  for (const uint32_t all = g.sums + g.zeros; g.base < all; g.base += kSumLaunch) {
+    const dim3 grid(all - g.base < kSumLaunch ? all - g.base : kSumLaunch), block(kSumWaves * kWave);
+    if (a.accumulate) embedding_sum_kernel<ET, GT, true><<<grid, block, 0, stream>>>(a, s, g);
+    else embedding_sum_kernel<ET, GT, false><<<grid, block, 0, stream>>>(a, s, g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.tokens <= kFold) return e;
+  if (a.tokens <= kFold) return hipSuccess;
   // a long run has more than kFold tokens
   const size_t join_slabs = (a.dim + kWave - 1) / kWave, items = a.tokens / (kFold + 1) * join_slabs;
   embedding_join_kernel<GT><<<dim3((unsigned)(items < 2048 ? items : 2048)), dim3(kJoinWaves * kWave), 0, stream>>>(

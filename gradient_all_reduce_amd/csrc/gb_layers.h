@@ -132,4 +132,17 @@ struct LookGradArgs {
 };
 hipError_t launch_embedding_grad(const LookGradArgs& a, hipStream_t stream);
 
+// The workgroups of the table's sums: [0, sums) add tokens, [sums, sums +
+// zeros) clear rows without one.  A launch takes those from base on, at most
+// kSumLaunch of them: a launch of 2^32 lanes would be refused, and 2^30 rows
+// of few columns, or 2^30 tokens, come to more.
+struct SumGrid {
+  size_t units;        // windows times slabs, a wavefront each
+  uint32_t slabs;      // of a row
+  uint32_t sums, zeros;  // multiples of the XCDs, as is base
+  uint32_t zero_each;  // rows a workgroup looks after
+  uint32_t base;
+};
+constexpr uint32_t kSumLaunch = 1u << 23;
+
 }  // namespace gb
