@@ -14,6 +14,8 @@
 // the sort, 8 the sums and 2 to 4 the join.
 #include "gb_rows.h"
 
+#define GB_LDS __attribute__((address_space(3)))
+
 namespace gb {
 namespace {
 
@@ -136,10 +138,12 @@ __device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
 
 // Ranks `items` (I at most) digits a lane within the wavefront, item i of the
 // lanes before item i + 1: rank[i] counts the equal digits before it, and
-// counts[digit] ends as their number.  counts: zeroed, this wavefront's own.
+// counts[digit] ends as their number.  counts: zeroed, this wavefront's own, in
+// LDS by its type: through a pointer of no address space volatile accesses are
+// flat ones, each of which waits for all of the wavefront's accesses to memory.
 template <int I>
 __device__ __forceinline__ void rank_wave(const uint32_t (&digit)[I], const bool (&valid)[I], uint32_t items,
-                                          uint32_t bits, volatile uint16_t* counts, uint32_t (&rank)[I]) {
+                                          uint32_t bits, volatile GB_LDS uint16_t* counts, uint32_t (&rank)[I]) {
 #pragma unroll
   for (int i = 0; i < I; i++) {
     if (i >= (int)items) break;
@@ -218,7 +222,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_small_kernel(LookGradArgs a
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSmallItems; i++) digit[i] = (key[i] >> (pass * d.bits)) & ((1u << d.bits) - 1u);
-    rank_wave<kSmallItems>(digit, valid, rounds, d.bits, counts[wave], rank);
+    rank_wave<kSmallItems>(digit, valid, rounds, d.bits, (GB_LDS uint16_t*)counts[wave], rank);
     __syncthreads();
     uint32_t sum = 0, c[kSortWaves];
 #pragma unroll
@@ -372,7 +376,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(LookGradArgs
       start[bin] = begin;
     }
     __syncthreads();
-    rank_wave<kTileItems>(digit, valid, kTileItems, p.bits, counts[wave], rank);
+    rank_wave<kTileItems>(digit, valid, kTileItems, p.bits, (GB_LDS uint16_t*)counts[wave], rank);
     __syncthreads();
     if (owner) {
       uint32_t in_tile = 0, c[kSortWaves];
