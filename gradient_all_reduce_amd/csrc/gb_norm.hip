@@ -191,10 +191,13 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
     const float rstd = 1.0f / sqrtf(team_sum<L, W>(square, var_part) * inv_n + a.eps);
     if (r < a.rows) {
       void* const row = row_at<ET, L>(a.y, r);
-      // With mean, rstd, weight and bias finite no value is NaN: a deviation
-      // times rstd is at most the root of cols, and a fused product and sum of
-      // finite numbers may overflow but has a sign.
-      if (__all(plain && finite(mean) && finite(rstd))) {
+      // With mean, weight and bias finite and rstd finite and above 0 no value
+      // is NaN: rstd is above 0 only if the sum of the squares is finite, so no
+      // deviation is infinite (one of a row of finite values may be: of 3.4e38
+      // and twice -3.4e38 the mean is -1.1e38).  A deviation times rstd is then
+      // at most the root of cols, and a fused product and sum of finite numbers
+      // may overflow but has a sign.
+      if (__all(plain && finite(mean) && finite(rstd) && rstd > 0.0f)) {
 #pragma unroll
         for (int k = 0; k < K; k++) {
           float y[V];

@@ -769,7 +769,10 @@ gb_status gb_adamw_step(const gb_optim_handle* plan, const void* control, void* 
  * cols 1 .. GB_NORM_MAX_COLS; eps finite and above 0 in binary32.  rows == 0
  * is GB_OK and enqueues nothing.  Forward and backward results agree with the
  * formulas up to the binary32 roundings of their sums; unlike the codecs' they
- * are not fixed bit for bit across versions of this library.
+ * are not fixed bit for bit across versions of this library.  Sums and squares
+ * that pass binary32 become infinite there: rows whose squared deviations do
+ * (values around 1e19 and up) have rstd 0, and y is the bias, or NaN where the
+ * deviation itself is infinite; a row whose sum does is NaN throughout.
  */
 gb_status gb_layer_norm_forward(int dtype, void* y, size_t y_stride, const void* x, size_t x_stride, size_t rows,
                                 size_t cols, int param_dtype, const void* weight, const void* bias, double eps,
