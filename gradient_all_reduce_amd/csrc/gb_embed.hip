@@ -123,7 +123,6 @@ __device__ __forceinline__ void token_rows(const LookGradArgs& a, const uint32_t
 __device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool valid, uint32_t bits) {
   const uint64_t all = __ballot(valid);
   uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
-#pragma unroll 2
   for (uint32_t b = 0; b < bits; b++) {
     const uint32_t mine = 0u - ((digit >> b) & 1u);  // all ones, or zeros
     const uint64_t set = __ballot(mine != 0u);

@@ -45,3 +45,11 @@ def test_no_access_is_a_flat_one(compiled, source):
     assert len(found) > 20
     flat = {name: re.findall(r"^\s+(flat_(?:load|store|atomic)\w*)", body, re.M) for name, body in found.items()}
     assert not {name: ops for name, ops in flat.items() if ops}
+
+
+@pytest.mark.parametrize("source", SOURCES)
+def test_the_compiler_follows_every_request(compiled, source):
+    """A pragma that cannot be followed is a warning: a loop whose ballots
+    stand under a condition of run time is not unrolled."""
+    warnings = [line for line in compiled[source][1].splitlines() if source in line and "warning:" in line]
+    assert not warnings
