@@ -830,6 +830,8 @@ def _layer_call(call, device, stream, *args):
     """One library call on the device's current stream, or the one given, with
     the device current: the null stream's handle names no device."""
     if stream is not None:
+        if stream.device_index != device:
+            raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{device}")
         handle = stream.cuda_stream
     elif _raw_stream is not None:
         handle = _raw_stream(device)
