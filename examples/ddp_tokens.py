@@ -26,7 +26,9 @@ PADDING = 0  # the id that fills short sequences: its row has no gradient
 
 
 class Embedding(torch.autograd.Function):
-    """Rows of the table times sqrt(width); the gradient goes to `bucket`."""
+    """Rows of the table times sqrt(width); the gradient goes to `bucket`.  The
+    anchor's value is not used: that it wants a gradient makes autograd come
+    back here."""
 
     @staticmethod
     def forward(ctx, anchor, table, ids, bucket, accumulate):
@@ -34,7 +36,7 @@ class Embedding(torch.autograd.Function):
         gb.gb_embedding_forward(out, table, ids, scale=math.sqrt(table.shape[1]))
         ctx.save_for_backward(ids)
         ctx.bucket, ctx.accumulate = bucket, accumulate
-        return out + anchor  # zero; makes autograd come back here
+        return out
 
     @staticmethod
     def backward(ctx, dout):
