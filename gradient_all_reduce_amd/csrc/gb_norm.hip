@@ -100,13 +100,13 @@ struct Team {
   }
 };
 
-// Row r of an array, or the last row for an r beyond it.  Where a wavefront
-// holds one row (L == 64) its address is a scalar.
-template <int ET, int L>
+// Row r of an array.
+template <int ET>
 __device__ __forceinline__ char* row_at(const Rows& a, size_t r) {
   return static_cast<char*>(a.p) + r * a.stride * Type<ET>::kSize;
 }
-// The team's number in the workgroup.
+// The team's number in the workgroup: a scalar where a wavefront belongs to
+// one team, and so are its rows' addresses.
 template <int L, int LANES>
 __device__ __forceinline__ uint32_t team_number() {
   const uint32_t t = threadIdx.x / LANES;
@@ -142,7 +142,7 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
 
   Raw<ET, V> x[K];
   auto load_row = [&](size_t r) {
-    const void* const row = row_at<ET, L>(a.x, r < a.rows ? r : a.rows - 1);
+    const void* const row = row_at<ET>(a.x, r < a.rows ? r : a.rows - 1);
 #pragma unroll
     for (int k = 0; k < K; k++) x[k] = t.load(row, k);
   };
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormArgs a) {
     }
     const float rstd = 1.0f / sqrtf(team_sum<L, W>(square, var_part) * inv_n + a.eps);
     if (r < a.rows) {
-      void* const row = row_at<ET, L>(a.y, r);
+      void* const row = row_at<ET>(a.y, r);
       // With mean, weight and bias finite and rstd finite and above 0 no value
       // is NaN: rstd is above 0 only if the sum of the squares is finite, so no
       // deviation is infinite (one of a row of finite values may be: of 3.4e38
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
   };
   auto load_row = [&](Row& row, size_t r) {
     r = r < a.rows ? r : a.rows - 1;
-    const void *const x_row = row_at<ET, L>(a.x, r), *const dy_row = row_at<ET, L>(a.dy, r);
+    const void *const x_row = row_at<ET>(a.x, r), *const dy_row = row_at<ET>(a.dy, r);
 #pragma unroll
     for (int k = 0; k < K; k++) {
       row.x[k] = t.load(x_row, k);
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs a) {
       }
     }
     if (r < a.rows) {
-      void* const to = row_at<ET, L>(a.dx, r);
+      void* const to = row_at<ET>(a.dx, r);
       // With both sums and rstd finite so are all g and h (an infinite one
       // would show in a sum), and fused products and sums of finite numbers
       // may overflow but have a sign: no value is NaN.
@@ -497,14 +497,20 @@ __global__ __launch_bounds__(kJoinLanes* kSlices) void norm_join_kernel(NormGrad
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-// Forward a workgroup is 512 lanes from 1025 columns of 2 bytes on, and 512
-// workgroups walk over the rows, two to a CU, with the parameters in registers
-// and the next row on its way.  16,384 x 8192 bfloat16: 512 workgroups 88.7 us,
-// 1024 96.9, 4096 92.5, one row each 121.  Eight wavefronts to a row rather than
-// four (91.5 us) or sixteen (90.8); over 4096 columns 46.5 us in eight, 47.4 in
-// four, 52 in one.  Up to 1024 columns 2048 workgroups of 256 lanes, or as many
-// as half as wide: 14.7 us over 16,384 x 1024, 19.5 with 512 of them.  Two rows
-// ahead instead of one: 17.5 there, level over longer rows.
+// Forward a workgroup is 512 lanes from 1025 columns of 2 bytes on (513 of 4),
+// and 512 workgroups walk over the rows, two to a CU, with the parameters in
+// registers and the next row on its way; beyond 8192 columns 256 workgroups of
+// 1024 lanes.  16,384 x 8192 bfloat16: 512 workgroups 88.7 us, 1024 96.9, 4096
+// 92.5, one row each 121.  Eight wavefronts to a row rather than four (91.5 us)
+// or sixteen (90.8); over 4096 columns 46.5 us in eight, 47.4 in four, 52 in
+// one.  Up to 1024 columns 2048 workgroups of 256 lanes: 14.7 us over 16,384 x
+// 1024, 19.5 with 512 workgroups.  Two rows ahead instead of one: 17.5 there,
+// level over longer rows.
+//
+// Beyond 16,384 columns a lane holds 32 columns, and its parameters, its row and
+// the next one no longer fit 128 registers: 120 (bfloat16) to 217 (float32)
+// spill.  8192 x 32,768 takes 230 us in bfloat16, 321 in float16 (161 at the
+// copy's rate) and 490 in float32 (323).
 template <int ET, int L, int W, int K, int THREADS, bool SHORT = false>
 hipError_t run_norm(const NormArgs& a, hipStream_t stream) {
   constexpr size_t kTeams = THREADS / (L * W), kMost = 512 * 512 / THREADS * (W > 2 ? 1 : 2);
@@ -539,8 +545,9 @@ hipError_t pick_norm(const NormArgs& a, hipStream_t stream) {
 // 79.1 us over 4096 columns.  A lane holds 8 columns of 2 bytes where 16
 // wavefronts suffice: with 16 columns h and g no longer fit beside the sums and
 // spill (5003 x 12,289 float16 255 us), so they are worked out again from the row
-// and the weights lie in LDS (103 us).  Beyond 16,384 columns the sums alone take
-// half the registers and some spill: 8192 x 32,768 bfloat16 takes 1.1 ms.
+// and the weights lie in LDS (103 us), which leaves 2 or 3 registers to spill.
+// Beyond 16,384 columns the sums alone take half the registers and 86 to 152
+// spill: 8192 x 32,768 takes 1.1 ms in 2 bytes a value, 2.1 in 4.
 template <int ET, int L, int W, int K, int THREADS, bool SHORT = false>
 struct NormGrad {
   static constexpr size_t kTeams = THREADS / (L * W), kMost = 256 * 1024 / THREADS;

@@ -53,3 +53,31 @@ def test_the_compiler_follows_every_request(compiled, source):
     stand under a condition of run time is not unrolled."""
     warnings = [line for line in compiled[source][1].splitlines() if source in line and "warning:" in line]
     assert not warnings
+
+
+def spills(text):
+    """(vector registers, bytes of scratch) that each kernel spills."""
+    found = {}
+    for part in re.findall(r"^  - \.agpr_count.*?\.wavefront_size", text, re.M | re.S):
+        value = {key: re.search(rf"\.{key}:\s+(\S+)", part).group(1)
+                 for key in ("name", "vgpr_spill_count", "private_segment_fixed_size")}
+        found[value["name"]] = int(value["vgpr_spill_count"]), int(value["private_segment_fixed_size"])
+    return found
+
+
+def test_only_the_widest_rows_spill(compiled):
+    """The layer norm's lanes hold K vectors of 16 bytes.  32 columns a lane
+    spill forward and backward; backward 16 columns spill 3 registers at most;
+    nothing else does."""
+    for name, (registers, scratch) in spills(compiled["gb_embed.hip"][0]).items():
+        assert (registers, scratch) == (0, 0), name
+    seen = 0
+    for name, (registers, scratch) in spills(compiled["gb_norm.hip"][0]).items():
+        m = re.search(r"(norm_kernel|norm_grad_kernel)ILi(\d)ELi\d+ELi\d+ELi(\d)E", name)
+        columns = int(m.group(3)) * (4 if m.group(2) == "0" else 8) if m else 0
+        seen += columns > 0
+        if columns == 16 and m.group(1) == "norm_grad_kernel":
+            assert registers <= 3 and scratch <= 16, name
+        elif columns < 32:
+            assert (registers, scratch) == (0, 0), name
+    assert seen == 2 * (12 + 11 + 11)
