@@ -750,9 +750,10 @@ gb_status gb_adamw_step(const gb_optim_handle* plan, const void* control, void* 
  * all may be views.  For the overlap rule an array reaches from its first
  * value to its last, the gaps between its rows included.  Types are
  * GB_DTYPE_F32, F16 or BF16 each; arithmetic is binary32 (the layer norm's with
- * fused multiply-adds), and an output is rounded to its type once.  Every NaN is stored as 0x7FC00000, or as that
- * NaN's rounding.  Calls with different workspaces may run at the same time;
- * two that share one belong on one stream, or ordered by events.
+ * fused multiply-adds), and an output is rounded to its type once.  Every NaN
+ * is stored as 0x7FC00000, or as that NaN's rounding.  Calls with different
+ * workspaces may run at the same time; two that share one belong on one
+ * stream, or ordered by events.
  * ------------------------------------------------------------------------- */
 
 /* Longest row of the layer norm calls. */
