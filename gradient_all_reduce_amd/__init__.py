@@ -827,8 +827,9 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 
 
 def _layer_call(call, device, stream, *args):
-    """One library call on the device's current stream, or the one given, with
-    the device current: the null stream's handle names no device."""
+    """One library call on the device's current stream, or the one given, which
+    has to be the device's, with the device current: the null stream's handle
+    names no device."""
     if stream is not None:
         if stream.device_index != device:
             raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{device}")

@@ -137,10 +137,10 @@ hipError_t launch_embedding_grad(const LookGradArgs& a, hipStream_t stream);
 // kSumLaunch of them: a launch of 2^32 lanes would be refused, and 2^30 rows
 // of few columns, or 2^30 tokens, come to more.
 struct SumGrid {
-  size_t units;        // windows times slabs, a wavefront each
-  uint32_t slabs;      // of a row
+  size_t units;          // windows times slabs, a wavefront each
+  uint32_t slabs;        // of a row
   uint32_t sums, zeros;  // multiples of the XCDs, as is base
-  uint32_t zero_each;  // rows a workgroup looks after
+  uint32_t zero_each;    // rows a workgroup looks after
   uint32_t base;
 };
 constexpr uint32_t kSumLaunch = 1u << 23;

@@ -499,9 +499,9 @@ __global__ __launch_bounds__(kJoinLanes* kSlices) void norm_join_kernel(NormGrad
 // ---------------------------------------------------------------------------
 // Forward a workgroup is 512 lanes from 1025 columns of 2 bytes on (513 of 4),
 // and 512 workgroups walk over the rows, two to a CU, with the parameters in
-// registers and the next row on its way; beyond 8192 columns 256 workgroups of
-// 1024 lanes.  16,384 x 8192 bfloat16: 512 workgroups 88.7 us, 1024 96.9, 4096
-// 92.5, one row each 121.  Eight wavefronts to a row rather than four (91.5 us)
+// registers and the next row on its way; beyond 8192 columns (4096 of 4 bytes)
+// 256 workgroups of 1024 lanes.  16,384 x 8192 bfloat16: 512 workgroups 88.7 us,
+// 1024 96.9, 4096 92.5, one row each 121.  Eight wavefronts to a row rather than four (91.5 us)
 // or sixteen (90.8); over 4096 columns 46.5 us in eight, 47.4 in four, 52 in
 // one.  Up to 1024 columns 2048 workgroups of 256 lanes: 14.7 us over 16,384 x
 // 1024, 19.5 with 512 workgroups.  Two rows ahead instead of one: 17.5 there,
